@@ -10,17 +10,28 @@ from .binding import (  # noqa: F401
     MoeError,
     MOE_OK,
     lib,
+    MOE_ACT,
+    moe_attn_dims,
+    moe_attn_forward,
+    moe_attn_workspace_bytes,
     moe_canonical_expert_bytes,
     moe_check_status,
     moe_dims,
     moe_dispatch,
     moe_experts_forward,
+    moe_kv_batch,
+    moe_kv_cache,
     moe_layer_forward,
     moe_layer_forward_host,
     moe_layer_forward_residual,
+    moe_linear,
+    moe_linear_workspace_bytes,
     moe_pack_q2,
     moe_packed_expert_bytes,
+    moe_qk_norm_rope,
     moe_rmsnorm_residual,
+    moe_rope,
+    moe_rope_init,
     moe_route,
     moe_route_noalloc,
     moe_set_cold_expert_tokens,

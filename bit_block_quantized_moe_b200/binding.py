@@ -36,6 +36,24 @@ class moe_shared(ctypes.Structure):
     _fields_ = [("packed", ctypes.c_void_p)]
 
 
+class moe_attn_dims(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
+
+
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int32)]
+
+
+class moe_kv_batch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
+
+
+class moe_rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("reserved", ctypes.c_int32), ("turn", ctypes.c_uint64 * 64)]
+
+
 EXPORTED = [
     "moe_canonical_expert_bytes",
     "moe_packed_expert_bytes",
@@ -49,6 +67,12 @@ EXPORTED = [
     "moe_experts_forward",
     "moe_dispatch",
     "moe_rmsnorm_residual",
+    "moe_linear_workspace_bytes",
+    "moe_linear",
+    "moe_rope_init",
+    "moe_attn_workspace_bytes",
+    "moe_qk_norm_rope",
+    "moe_attn_forward",
     "moe_trace_kernel",
     "moe_set_cold_expert_tokens",
     "moe_check_status",
@@ -94,6 +118,20 @@ def lib():
         L.moe_dispatch.argtypes = [D, P, i32, P, P, P, P, P, sz, P]
         L.moe_rmsnorm_residual.restype = ctypes.c_int
         L.moe_rmsnorm_residual.argtypes = [P, P, P, i32, i32, ctypes.c_float, P]
+        i64, f32, A = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(moe_attn_dims)
+        C, S = ctypes.POINTER(moe_kv_cache), ctypes.POINTER(moe_kv_batch)
+        L.moe_linear_workspace_bytes.restype = sz
+        L.moe_linear_workspace_bytes.argtypes = [i32, i32, i32]
+        L.moe_linear.restype = ctypes.c_int
+        L.moe_linear.argtypes = [P, i64, P, P, ctypes.c_int, P, P, i32, i32, i32, P, sz, P]
+        L.moe_rope_init.restype = ctypes.c_int
+        L.moe_rope_init.argtypes = [ctypes.c_double, i32, ctypes.POINTER(moe_rope)]
+        L.moe_attn_workspace_bytes.restype = sz
+        L.moe_attn_workspace_bytes.argtypes = [A, i32, i32]
+        L.moe_qk_norm_rope.restype = ctypes.c_int
+        L.moe_qk_norm_rope.argtypes = [A, P, i64, P, P, f32, ctypes.POINTER(moe_rope), C, S, i32, P, P, sz, P]
+        L.moe_attn_forward.restype = ctypes.c_int
+        L.moe_attn_forward.argtypes = [A, P, i64, C, S, i32, f32, i32, i32, P, P, sz, P]
         L.moe_trace_kernel.restype = ctypes.c_int
         L.moe_trace_kernel.argtypes = [i32, P, P]
         L.moe_set_cold_expert_tokens.restype = ctypes.c_int
@@ -233,9 +271,132 @@ def moe_rmsnorm_residual(resid, y, x_norm, T: int, hidden: int, eps: float = 1e-
     _check(code, "moe_rmsnorm_residual")
 
 
+MOE_ACT = {"none": 0, "silu": 1, "gelu": 2}
+
+
+def _here(what, *tensors):
+    """Refuses tensors that are not on the current CUDA device (the call launches there)."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{what}: every tensor belongs on the current CUDA device")
+
+
+def _half(what, *tensors):
+    """Refuses what is not bf16 (or its bit patterns in 16-bit integers)."""
+    for t in tensors:
+        if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+            raise ValueError(f"{what}: activations, weights and caches are bf16")
+
+
+def moe_linear_workspace_bytes(max_T: int, K: int, N: int) -> int:
+    return int(lib().moe_linear_workspace_bytes(int(max_T), int(K), int(N)))
+
+
+def moe_linear(x, w, out, workspace, bias=None, act="none", resid=None, stream=None):
+    """out = act(x w^T + bias) in bf16, or resid + that in fp32 (out may be resid).  x [T, K] bf16 (rows may be
+    strided), w [N, K] bf16, bias [N] fp32, resid and out [T, N]."""
+    _here("moe_linear", x, w, out, workspace, bias, resid)
+    _half("moe_linear", x, w)
+    T, K = x.shape
+    N = w.shape[0]
+    f32 = torch.float32
+    if w.shape[1] != K or out.shape != (T, N) or (bias is not None and (bias.numel() != N or bias.dtype != f32)) or (
+            resid is not None and (resid.shape != (T, N) or resid.dtype != f32)):
+        raise ValueError("moe_linear: shapes or types do not match")
+    if act not in MOE_ACT or (out.dtype != f32 if resid is not None else out.element_size() != 2):
+        raise ValueError("moe_linear: out is bf16, or fp32 with a residual; act is none, silu or gelu")
+    if x.stride(1) != 1 or not (w.is_contiguous() and out.is_contiguous() and (bias is None or bias.is_contiguous())
+                                and (resid is None or resid.is_contiguous())):
+        raise ValueError("moe_linear: only the rows of x may be strided")
+    code = lib().moe_linear(x.data_ptr(), x.stride(0) if T > 1 else K, w.data_ptr(), _ptr(bias), MOE_ACT[act],
+                            _ptr(resid), out.data_ptr(), T, K, N, workspace.data_ptr(), workspace.nbytes,
+                            _stream(stream))
+    _check(code, "moe_linear")
+
+
+def moe_rope_init(theta: float, rotary_dim: int) -> moe_rope:
+    rope = moe_rope()
+    _check(lib().moe_rope_init(float(theta), int(rotary_dim), ctypes.byref(rope)), "moe_rope_init")
+    return rope
+
+
+def moe_attn_workspace_bytes(dims: moe_attn_dims, n_seqs: int, max_T: int) -> int:
+    return int(lib().moe_attn_workspace_bytes(ctypes.byref(dims), int(n_seqs), int(max_T)))
+
+
+def _cache_and_batch(what, dims, k_cache, v_cache, kv_len, page_table, q_start):
+    shape = k_cache.shape
+    if shape[1:] != (dims.n_kv_heads, dims.page_size, dims.head_dim) or v_cache.shape != shape or not (
+            k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError(f"{what}: k and v are contiguous [n_pages, n_kv_heads, page_size, head_dim]")
+    _half(what, k_cache, v_cache)
+    n = kv_len.shape[0]
+    i32 = torch.int32
+    if page_table.shape[0] != n or page_table.dtype != i32 or kv_len.dtype != i32 or not (
+            page_table.is_contiguous() and kv_len.is_contiguous()) or (q_start is not None and (
+                q_start.shape[0] != n + 1 or q_start.dtype != i32 or not q_start.is_contiguous())):
+        raise ValueError(f"{what}: kv_len [n_seqs], page_table [n_seqs, max_pages], q_start [n_seqs + 1], contiguous "
+                         "int32")
+    return (moe_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), shape[0]),
+            moe_kv_batch(n, page_table.shape[1], _ptr(q_start), kv_len.data_ptr(), page_table.data_ptr()))
+
+
+def _token_rows(what, t, heads, dim):
+    """Elements between neighbouring tokens of t, [T, heads, dim] or [T, heads * dim]."""
+    if t.dim() == 3:
+        ok = t.shape[1] == heads and t.shape[2] == dim and t.stride(2) == 1 and (heads == 1 or t.stride(1) == dim)
+    else:
+        ok = t.dim() == 2 and t.shape[1] == heads * dim and t.stride(1) == 1
+    if not ok:
+        raise ValueError(f"{what} [T, {heads}, {dim}], every token contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def moe_qk_norm_rope(dims, qkv, q_out, k_cache, v_cache, kv_len, page_table, workspace, rope=None, q_start=None,
+                     q_gain=None, k_gain=None, eps=1e-6, stream=None):
+    """Per-head norms and rotation of qkv [T, (n_heads + 2 n_kv_heads) * head_dim]; queries to q_out [T, n_heads,
+    head_dim], keys and values to their pages."""
+    what = "moe_qk_norm_rope"
+    _here(what, qkv, q_out, k_cache, v_cache, kv_len, page_table, workspace, q_start, q_gain, k_gain)
+    _half(what, qkv, q_out)
+    cache, batch = _cache_and_batch(what, dims, k_cache, v_cache, kv_len, page_table, q_start)
+    ld = _token_rows("moe_qk_norm_rope: qkv", qkv, dims.n_heads + 2 * dims.n_kv_heads, dims.head_dim)
+    T = qkv.shape[0]
+    if q_out.shape[0] != T or q_out.numel() != T * dims.n_heads * dims.head_dim or not q_out.is_contiguous():
+        raise ValueError("moe_qk_norm_rope: q_out is contiguous [T, n_heads, head_dim]")
+    for gain in (q_gain, k_gain):
+        if gain is not None and (gain.dtype != torch.float32 or gain.numel() != dims.head_dim
+                                 or not gain.is_contiguous()):
+            raise ValueError("moe_qk_norm_rope: gains are [head_dim] fp32")
+    code = lib().moe_qk_norm_rope(ctypes.byref(dims), qkv.data_ptr(), ld, _ptr(q_gain), _ptr(k_gain), eps,
+                                  None if rope is None else ctypes.byref(rope), ctypes.byref(cache),
+                                  ctypes.byref(batch), T, q_out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                  _stream(stream))
+    _check(code, what)
+
+
+def moe_attn_forward(dims, q, out, k_cache, v_cache, kv_len, page_table, workspace, q_start=None, scale=None, window=0,
+                     n_sinks=0, stream=None):
+    """Attention of q [T, n_heads, head_dim] (tokens may be strided) over the paged cache; scale defaults to
+    head_dim ** -0.5."""
+    what = "moe_attn_forward"
+    _here(what, q, out, k_cache, v_cache, kv_len, page_table, workspace, q_start)
+    _half(what, q, out)
+    cache, batch = _cache_and_batch(what, dims, k_cache, v_cache, kv_len, page_table, q_start)
+    ld = _token_rows("moe_attn_forward: q", q, dims.n_heads, dims.head_dim)
+    T = q.shape[0]
+    if out.shape[0] != T or out.numel() != T * dims.n_heads * dims.head_dim or not out.is_contiguous():
+        raise ValueError("moe_attn_forward: out is contiguous [T, n_heads, head_dim]")
+    code = lib().moe_attn_forward(ctypes.byref(dims), q.data_ptr(), ld, ctypes.byref(cache), ctypes.byref(batch), T,
+                                  dims.head_dim ** -0.5 if scale is None else scale, window, n_sinks, out.data_ptr(),
+                                  workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    _check(code, what)
+
+
 MOE_KERNEL = {"router_logits": 0, "topk": 1, "dispatch_bits": 2, "dispatch_scan": 3, "dispatch_place": 4,
               "gate_up": 5, "down": 6, "combine": 7, "decode_fused": 8,
-              "gather": 9}
+              "gather": 9, "linear": 10, "qk_norm": 11, "attn": 12}
 
 
 def moe_trace_kernel(kernel_id: int, before=None, after=None):

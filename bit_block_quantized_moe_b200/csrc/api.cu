@@ -121,7 +121,7 @@ void trace_mark(int id, bool after, cudaStream_t s) {
 
 static moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
-static moe_status device_ok() {
+moe_status device_ok() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   int major = 0;

@@ -1,0 +1,73 @@
+// Shared by the attention kernels: what they know of a batch, and small device helpers.
+#pragma once
+
+#include <limits.h>
+
+#include "attn_index.h"
+#include "kernels.cuh"
+
+namespace moe {
+
+struct KvArgs {
+  const int32_t *q_start, *kv_len, *table;
+  int n_seqs, max_pages, n_pages;
+  int per;     // rows a sequence when q_start is null
+  int cap;     // max_pages * page_size
+  int log_ps;  // log2(page_size)
+};
+
+cudaError_t launch_qk_norm_rope(const moe_attn_dims &d, const uint16_t *qkv, int64_t ld, const float *gq,
+                                const float *gk, float eps, const moe_rope *rope, const moe_kv_cache &c,
+                                const KvArgs &kv, int T, uint16_t *q_out, uint32_t *status, cudaStream_t s);
+
+struct AttnArgs {
+  const uint16_t *q;
+  int64_t ld_q;
+  const uint16_t *k, *v;
+  KvArgs kv;
+  int H, V, G, T;
+  float scale_log2;  // scale * log2(e)
+  int window, n_sinks;
+  uint16_t *out;
+  uint32_t *status;
+  float *part;  // workspace: parts of split sequences
+};
+
+size_t attn_part_bytes(const moe_attn_dims &d, int n_seqs, int T);
+cudaError_t launch_attn(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s);
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void unpack8(const uint4 &r, float (&x)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
+}
+
+// The sequence of row t, by a whole warp: the number of ends at or before t when the starts do not decrease (the
+// caller checks that t lies in that sequence), -1 past the last.
+__device__ __forceinline__ int seq_of_row(const KvArgs &kv, int t, int lane) {
+  if (!kv.q_start) return t / kv.per;
+  int c = 0;
+  for (int b = lane; b < kv.n_seqs; b += 32) c += __ldg(kv.q_start + b + 1) <= t;
+  c = __reduce_add_sync(0xffffffffu, c);
+  return c < kv.n_seqs ? c : -1;
+}
+
+// One CTA's threads look the sequences over and report what is out of range.
+__device__ __forceinline__ void check_sequences(const KvArgs &kv, int T, uint32_t *status) {
+  bool bad = false;
+  for (int b = threadIdx.x; b < kv.n_seqs; b += blockDim.x)
+    bad |= seq_view(kv.q_start, kv.kv_len, b, kv.per, T, kv.cap).bad;
+  if (bad) set_status(status, kStatusBadIndex);
+}
+#endif
+
+}  // namespace moe

@@ -44,6 +44,9 @@ struct Workspace {
 // Profiling hook (moe_trace_kernel): records the caller's events around kernel `id`.
 void trace_mark(int id, bool after, cudaStream_t s);
 
+// MOE_OK when the current device is one this library runs on (compute capability 10.x).
+moe_status device_ok();
+
 size_t workspace_layout(const moe_dims &d, int T, void *base, Workspace *ws);
 
 cudaError_t launch_pack(const uint8_t *canon, uint8_t *packed, int n_experts, const PackedGeom &G,
@@ -85,5 +88,10 @@ cudaError_t launch_combine_rmsnorm(const moe_dims &d, int T, const Workspace &ws
 constexpr int kHostIoMaxTokens = 8;
 cudaError_t launch_stream_copy16(const void *src, void *dst, size_t bytes, cudaStream_t s);
 void *mapped_host_range(const void *p, size_t bytes);
+// Matrix product with its epilogue (linear.cu); `part` holds linear_part_bytes() for the K-split parts.
+size_t linear_part_bytes();
+cudaError_t launch_linear(const uint16_t *x, int64_t ld, const uint16_t *w, const float *bias, int act,
+                          const float *resid, void *out, int T, int K, int N, float *part, uint32_t *status,
+                          cudaStream_t s);
 
 }  // namespace moe

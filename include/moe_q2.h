@@ -279,6 +279,121 @@ moe_status moe_dispatch(const moe_dims *dims, const int32_t *topk_idx, int32_t T
 moe_status moe_rmsnorm_residual(float *resid, const uint16_t *y, uint16_t *x_norm, int32_t T, int32_t hidden,
                                 float eps, moe_stream_t stream);
 
+/* ---- the attention half of a decoder layer ----------------------------------------------
+ * What a stack of layers runs between two MoE calls.  With x_norm the bf16 rows that
+ * moe_rmsnorm_residual / moe_layer_forward_residual leave and resid the fp32 residual:
+ *   moe_linear          qkv = x_norm Wqkv^T + b
+ *   moe_qk_norm_rope    per-head norms and rotation of q and k; k and v into the pages of the cache
+ *   moe_attn_forward    o = attention of q over the cache
+ *   moe_linear          resid += o Wo^T
+ *   moe_rmsnorm_residual(resid, NULL, x_norm), then the MoE half.
+ * Calls are asynchronous, allocate nothing, and take a workspace whose first 256
+ * bytes follow the rules of moe_workspace_bytes (sticky status word, zeroed once
+ * after allocation and again after MOE_ERR_TIMEOUT; not shared by calls that can
+ * run at the same time; read with moe_check_status). */
+
+/* Matrix product with its epilogue: z = x w^T + bias (exact bf16 products, fp32
+ * sums), a = act(z), then
+ *   resid == NULL:  out [T, N] bf16 = a (nearest even);
+ *   resid != NULL:  out [T, N] fp32 = resid + a; out may be resid itself (in place),
+ *                   and must not overlap it in any other way.
+ * x [T, K] bf16 with ld_x elements between rows, w [N, K] bf16 row-major, bias [N]
+ * fp32 or NULL, resid [T, N] fp32.  silu(z) = z / (1 + exp(-z)), gelu(z) =
+ * z/2 (1 + erf(z / sqrt 2)).  K and ld_x are multiples of 8, 8 <= K <= 65536,
+ * 1 <= N <= 262144, ld_x >= K; x, w, bias, resid and out 16-byte aligned.  Out may not overlap
+ * x, w or bias.  T = 0 is a no-op. */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2 } moe_act;
+/* Host.  Workspace bytes of moe_linear for every T <= max_T (0 if invalid). */
+size_t moe_linear_workspace_bytes(int32_t max_T, int32_t K, int32_t N);
+moe_status moe_linear(const uint16_t *x, int64_t ld_x, const uint16_t *w, const float *bias, moe_act act,
+                      const float *resid, void *out, int32_t T, int32_t K, int32_t N, void *workspace,
+                      size_t ws_bytes, moe_stream_t stream);
+
+/* Attention shapes: n_heads query heads in groups of n_heads / n_kv_heads that share
+ * a key/value head (query head h reads key/value head h / group); head_dim 64 or 128;
+ * page_size 16, 32, 64 or 128 tokens; n_heads <= 1024 and group <= 128. */
+typedef struct {
+  int32_t n_heads;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+} moe_attn_dims;
+
+/* The paged cache: k and v, each [n_pages, n_kv_heads, page_size, head_dim] bf16,
+ * 16-byte aligned; n_pages * n_kv_heads * page_size < 2^31. */
+typedef struct {
+  uint16_t *k;
+  uint16_t *v;
+  int32_t n_pages;
+} moe_kv_cache;
+
+/* The sequences of a call (device arrays).  Sequence b brings the new tokens in rows
+ * q_start[b] .. q_start[b + 1] - 1 (q_start == NULL: T / n_seqs rows each, T a multiple
+ * of n_seqs) and has kv_len[b] tokens in all, the new ones last: new token i of m
+ * stands at position kv_len[b] - m + i.  The token at position p lives in page
+ * page_table[b * max_pages + p / page_size], row p % page_size; entries past the
+ * sequence's last page are never read.  1 <= n_seqs <= 65536, 1 <= max_pages,
+ * max_pages * page_size <= 2^30.
+ * A sequence with kv_len[b] = 0 is padding: its rows stand at negative positions.
+ * Rows of no sequence (before q_start[0], at or after q_start[n_seqs]) are left as they
+ * were.  What the device finds wrong sets MOE_ERR_DEVICE in the workspace status: a
+ * q_start pair that decreases or leaves [0, T] makes that sequence empty, a kv_len
+ * outside [0, max_pages * page_size] counts as 0, and a token whose page is outside
+ * [0, n_pages) is neither written nor seen. */
+typedef struct {
+  int32_t n_seqs;
+  int32_t max_pages;
+  const int32_t *q_start;
+  const int32_t *kv_len;
+  const int32_t *page_table;
+} moe_kv_batch;
+
+/* Rotation of the first rotary_dim elements of a head by pairs (i, i + rotary_dim/2),
+ * angle position * theta^(-2i / rotary_dim).  turn[i] is that frequency in turns per
+ * position, as a 64-bit fixed-point fraction, so that position * turn[i] (mod 2^64) is
+ * the angle mod one turn at any position.  rotary_dim is a multiple of 16 up to
+ * head_dim (at most 128), theta >= 1.  Filled by moe_rope_init (host). */
+typedef struct {
+  int32_t rotary_dim;
+  int32_t reserved;
+  uint64_t turn[64];
+} moe_rope;
+moe_status moe_rope_init(double theta, int32_t rotary_dim, moe_rope *rope);
+
+/* Host.  Workspace bytes of moe_qk_norm_rope and moe_attn_forward for up to n_seqs
+ * sequences and every T <= max_T (0 if invalid). */
+size_t moe_attn_workspace_bytes(const moe_attn_dims *dims, int32_t n_seqs, int32_t max_T);
+
+/* One pass over the projections of T new tokens, qkv [T, (n_heads + 2 n_kv_heads) *
+ * head_dim] bf16 (query heads, key heads, value heads; ld_qkv elements between rows, a
+ * multiple of 8).  For each query and key head h: h / sqrt(mean(h^2) + eps) * gain,
+ * then the rotation at the token's position, in fp32 and rounded once.  Queries go to
+ * q_out [T, n_heads, head_dim] bf16, keys and (unchanged) values to their rows of the
+ * cache.  q_gain, k_gain [head_dim] fp32 or NULL (unit gain); rope NULL: no rotation.
+ * A row at a negative position gets zero queries and writes no key or value.  The
+ * cached rows of two tokens of one call must be distinct. */
+moe_status moe_qk_norm_rope(const moe_attn_dims *dims, const uint16_t *qkv, int64_t ld_qkv, const float *q_gain,
+                            const float *k_gain, float eps, const moe_rope *rope, const moe_kv_cache *cache,
+                            const moe_kv_batch *batch, int32_t T, uint16_t *q_out, void *workspace, size_t ws_bytes,
+                            moe_stream_t stream);
+
+/* Attention of T new tokens over the cache that already holds them: the query at
+ * position i sees key j when j <= i and, with window > 0, also i - j < window or
+ * j < n_sinks (the first n_sinks tokens stay visible);
+ *   out = sum_j softmax_j(scale q.k_j) v_j,
+ * scores and sums in fp32, the weights rounded to bf16 for the product with v.  q
+ * [T, n_heads, head_dim] bf16 with ld_q elements between rows (a multiple of 8), out
+ * [T, n_heads, head_dim] bf16 contiguous.  A row that sees nothing is written as zeros.
+ * What lies in cache rows that a query does not see (any bits, NaN among them) does not
+ * reach its output; a non-finite v that it sees may make its whole output row NaN.
+ * window = 0: all earlier tokens; n_sinks >= 0 (without a window it changes nothing).
+ * Which kernel runs: q_start == NULL and T <= 8 n_seqs (verify windows) splits each
+ * sequence's cached length over the SMs and joins the parts; anything else (prompt
+ * chunks) takes tiles of queries. */
+moe_status moe_attn_forward(const moe_attn_dims *dims, const uint16_t *q, int64_t ld_q, const moe_kv_cache *cache,
+                            const moe_kv_batch *batch, int32_t T, float scale, int32_t window, int32_t n_sinks,
+                            uint16_t *out, void *workspace, size_t ws_bytes, moe_stream_t stream);
+
 /* ---- profiling aid ------------------------------------------------------------------
  * While kernel_id >= 0, every later call made by this host thread records the
  * CUDA event `before` (a cudaEvent_t created by the caller) on its stream just
@@ -297,7 +412,10 @@ enum {
   MOE_KERNEL_DOWN = 6,
   MOE_KERNEL_COMBINE = 7,
   MOE_KERNEL_DECODE_FUSED = 8,
-  MOE_KERNEL_GATHER = 9
+  MOE_KERNEL_GATHER = 9,
+  MOE_KERNEL_LINEAR = 10,
+  MOE_KERNEL_QK_NORM = 11,
+  MOE_KERNEL_ATTN = 12
 };
 moe_status moe_trace_kernel(int32_t kernel_id, void *before, void *after);
 
