@@ -368,10 +368,13 @@ cudaError_t launch_d(const WinArgs &w, cudaStream_t s) {
 // Parts exist only where a window is split, in at most kWave CTAs of at most 64 rows.
 size_t attn_part_bytes(const moe_attn_dims &d, int, int) { return (size_t)kWave * 64 * (d.head_dim + 2) * 4; }
 
-cudaError_t launch_attn(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &, cudaStream_t s) {
+cudaError_t launch_attn(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) {
   WinArgs w{a, 1, 1};
   trace_mark(MOE_KERNEL_ATTN, false, s);
-  const cudaError_t err = d.head_dim == 128 ? launch_d<128>(w, s) : launch_d<64>(w, s);
+  const bool window = !a.kv.q_start && a.kv.per <= 8;
+  const cudaError_t err = !window             ? launch_attn_tc(d, a, c, s)
+                          : d.head_dim == 128 ? launch_d<128>(w, s)
+                                              : launch_d<64>(w, s);
   trace_mark(MOE_KERNEL_ATTN, true, s);
   return err;
 }

@@ -34,6 +34,7 @@ struct AttnArgs {
 };
 
 size_t attn_part_bytes(const moe_attn_dims &d, int n_seqs, int T);
+cudaError_t launch_attn_tc(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s);
 cudaError_t launch_attn(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s);
 
 #ifdef __CUDACC__

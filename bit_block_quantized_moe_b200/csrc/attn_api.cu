@@ -166,9 +166,12 @@ moe_status moe_attn_forward(const moe_attn_dims *dims, const uint16_t *q, int64_
   a.V = dims->n_kv_heads;
   a.G = a.H / a.V;
   a.T = T;
+  // scale 0 weighs all seen keys alike, as this does, and keeps masked scores at -inf
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.window = window;
-  a.n_sinks = n_sinks;
+  if (a.scale_log2 == 0.f) a.scale_log2 = 1e-37f;
+  // positions stay below 2^30
+  a.window = window < (1 << 30) ? window : 1 << 30;
+  a.n_sinks = n_sinks < (1 << 30) ? n_sinks : 1 << 30;
   a.out = out;
   a.status = reinterpret_cast<uint32_t *>(ws);
   a.part = reinterpret_cast<float *>(ws + kWsHeader);

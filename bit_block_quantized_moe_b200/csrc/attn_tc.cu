@@ -1,0 +1,509 @@
+// Attention of prompt chunks over the paged cache on the 5th-generation tensor cores (tcgen05, sm_100a).
+//
+// A CTA takes one key/value head of one sequence and up to two tiles of 128 rows; a tile's rows are (token, head of
+// the group) pairs, so that all heads of a group share the keys that were loaded for one.  It walks the 128-key
+// tiles that its rows see.  For each of its row tiles i and key tile j, with the softmax's running maximum m and sum l:
+//   S_i = Q_i K_j^T            (tensor memory, fp32)
+//   P_i = 2^(scale S_i - m)    (one thread a row; bf16, over S_i in tensor memory)
+//   O_i += P_i V_j             (tensor memory, fp32)
+// The products of one row tile run under the softmax of the other.  m is the maximum seen so far, left as it is
+// until a row exceeds it by 8 (a factor of 256, which fp32 sums and bf16 weights carry without loss: only then are l
+// and O_i, which lie in tensor memory, rescaled), so that the rescaling is rare.
+//   warps 0-3, 4-7 : softmax of row tile 0, 1, then its output rows;
+//   warp 8         : TMA: queries once, K and V a page at a time, into rings of 128-key stages;
+//   warp 9         : tcgen05.mma issue;
+//   warps 10, 11   : V rows that must not be multiplied (keys that no row sees, non-finite values behind a mask)
+//                    are cleared before P V, in tiles with a mask only.
+// Every wait is bounded (sync.cuh).
+#include <algorithm>
+
+#include "attn.cuh"
+#include "tc.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTcBK = 128;   // keys a tile
+constexpr int kTcLogBK = 7;
+constexpr int kTcRows = 128;
+constexpr int kTcThreads = 384;
+constexpr int kTcInfo = 8;   // ring of tile descriptions: more than the tiles between the producer and a softmax
+constexpr float kTcLazy = 8.0f;
+
+template <int D>
+struct TcCfg {
+  static constexpr int kHalves = D / 64;                    // 64-column halves of a row (one swizzle row each)
+  static constexpr int kHalfBytes = 128 * 128;              // 128 rows x 64 columns
+  static constexpr int kTileBytes = kHalves * kHalfBytes;   // a Q, K or V tile
+  static constexpr int kStages = 2;                         // K and V stages each
+  static constexpr int kSmemTiles = 2 + 2 * kStages;
+  static constexpr uint32_t kS = 0, kO = 256;               // tensor memory columns: S0 S1, O0 O1
+  static constexpr uint32_t kTmemCols = 512;
+};
+
+struct TileInfo {
+  int partial;       // some row does not see some key of the tile
+  uint32_t bad[4];   // keys whose page is outside the cache
+};
+
+template <int D>
+struct TcBars {
+  uint64_t q_full, k_full[TcCfg<D>::kStages], k_empty[TcCfg<D>::kStages], v_full[TcCfg<D>::kStages],
+      v_ready[TcCfg<D>::kStages], v_empty[TcCfg<D>::kStages], s_full[2], p_ready[2], pv_done[2], done;
+  TileInfo info[kTcInfo];
+  uint32_t flagged[TcCfg<D>::kStages][4];  // keys of a V stage whose values are not finite
+  uint32_t tmem;
+  int abort;
+  int found_b, found_t, warp_sum[kTcThreads / 32];
+};
+
+struct TcArgs {
+  AttnArgs a;
+  int tokens;  // tokens a row tile: 128 / G
+};
+
+template <class Bars>
+__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, Bars &B, uint32_t *status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  if (*reinterpret_cast<volatile int *>(&B.abort)) return false;
+  if (!mbar_wait(bar, parity)) {
+    set_status(status, kStatusTimeout);
+    B.abort = 1;
+    return false;
+  }
+  return true;
+}
+
+// B operand with N contiguous (V: keys x head_dim): 64-column groups kHalfBytes apart, 8-key groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_n_sw128(uint32_t addr, uint32_t group_bytes) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(group_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TcArgs w) {
+  using C = TcCfg<D>;
+  extern __shared__ __align__(1024) uint8_t tc_raw[];
+  uint8_t *smem = tc_raw + ((1024u - (smem_u32(tc_raw) & 1023u)) & 1023u);
+  uint8_t *q_s = smem, *k_s = smem + 2 * C::kTileBytes, *v_s = k_s + C::kStages * C::kTileBytes;
+  TcBars<D> &B = *reinterpret_cast<TcBars<D> *>(smem + C::kSmemTiles * C::kTileBytes);
+  const AttnArgs &a = w.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hv = blockIdx.x % a.V, item = blockIdx.x / a.V;
+
+  // ---- which rows: items count row-tile pairs from the last sequence's last pair (with a causal mask the largest)
+  if (blockIdx.x == 0) check_sequences(a.kv, a.T, a.status);
+  if (threadIdx.x == 0) B.found_b = -1;
+  __syncthreads();
+  const int pair = 2 * w.tokens;
+  for (int c0 = 0, base = 0; c0 < a.kv.n_seqs; c0 += kTcThreads) {
+    const int b = a.kv.n_seqs - 1 - (c0 + (int)threadIdx.x);
+    const int cnt = b >= 0 ? (seq_view(a.kv.q_start, a.kv.kv_len, b, a.kv.per, a.T, a.kv.cap).m + pair - 1) / pair : 0;
+    int incl = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) B.warp_sum[warp] = incl;
+    __syncthreads();
+    int before = base, total = 0;
+    for (int i = 0; i < kTcThreads / 32; ++i) {
+      if (i < warp) before += B.warp_sum[i];
+      total += B.warp_sum[i];
+    }
+    const int at = item - (before + incl - cnt);
+    if (at >= 0 && at < cnt) {
+      B.found_b = b;
+      B.found_t = cnt - 1 - at;
+    }
+    base += total;
+    __syncthreads();
+    if (item < base) break;
+  }
+  const int b = B.found_b;
+  if (b < 0) return;
+  const SeqView s = seq_view(a.kv.q_start, a.kv.kv_len, b, a.kv.per, a.T, a.kv.cap);
+  const int tok0 = B.found_t * pair;
+  const int nq = s.m - tok0 > w.tokens ? 2 : 1;
+  const int base = s.n - s.m;
+  const int p0 = base + tok0, p1 = base + min(s.m, tok0 + pair) - 1;
+  const TileRange tr = tile_range(p0, p1, s.n, a.window, a.n_sinks, kTcLogBK);
+  const int nt = tr.count;
+  const int32_t *table = a.kv.table + (size_t)b * a.kv.max_pages;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&B.q_full, 1);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&B.k_full[i], 1);
+      mbar_init(&B.k_empty[i], 1);
+      mbar_init(&B.v_full[i], 1);
+      mbar_init(&B.v_ready[i], 2);
+      mbar_init(&B.v_empty[i], 3);  // the products' commit and the two clearing warps
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B.s_full[i], 1);
+      mbar_init(&B.p_ready[i], 4);
+      mbar_init(&B.pv_done[i], 1);
+    }
+    mbar_init(&B.done, 1);
+    B.abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 9) tmem_alloc(&B.tmem, C::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = B.tmem;
+
+  if (warp == 8) {
+    // ---- producer ----
+    const int rows = w.tokens * a.G;
+    if (nt > 0 && elect_one()) {
+      mbar_arrive_expect_tx(&B.q_full, (uint32_t)(nq * C::kHalves * rows * 128));
+      for (int i = 0; i < nq; ++i)
+        for (int h = 0; h < C::kHalves; ++h)
+          tma_load_3d(q_s + i * C::kTileBytes + h * C::kHalfBytes, &qmap, h * 64, hv * a.G, s.q0 + tok0 + i * w.tokens,
+                      &B.q_full);
+    }
+    __syncwarp();
+    const int ps = 1 << a.kv.log_ps, pages = kTcBK >> a.kv.log_ps;
+    bool live = true;
+    int issued_k = 0, issued_v = 0;
+    for (int t = 0; t < nt; ++t) {
+      const int st = t % C::kStages, j0 = tile_of(tr, t) << kTcLogBK;
+      const uint32_t ph = ((t / C::kStages) & 1) ^ 1;
+      if (live && !at_wait(&B.k_empty[st], ph, B, a.status)) live = false;
+      if (!live) break;
+      // lane l < pages: page l of the tile
+      const int a0 = j0 + (lane << a.kv.log_ps), e0 = a0 + ps;
+      const bool seen = lane < pages && a0 < s.n && a0 <= p1 &&
+                        (a.window <= 0 || e0 - 1 > p0 - a.window || a0 < a.n_sinks);
+      const int page = seen ? __ldg(table + (a0 >> a.kv.log_ps)) : 0;
+      const bool ok = seen && page >= 0 && page < a.kv.n_pages;
+      const uint32_t good = __ballot_sync(0xffffffffu, ok), wrong = __ballot_sync(0xffffffffu, seen && !ok);
+      if (lane == 0) {
+        TileInfo &in = B.info[t % kTcInfo];
+        in.partial = wrong || !tile_full(p0, p1, j0, kTcBK, s.n, a.window, a.n_sinks);
+        in.bad[0] = in.bad[1] = in.bad[2] = in.bad[3] = 0;
+        if (wrong) {
+          for (int k = 0; k < kTcBK; ++k)
+            if (wrong >> (k >> a.kv.log_ps) & 1) in.bad[k >> 5] |= 1u << (k & 31);
+          set_status(a.status, kStatusBadIndex);
+        }
+        mbar_arrive_expect_tx(&B.k_full[st], (uint32_t)(__popc(good) * ps * D * 2));
+      }
+      __syncwarp();
+      const int row = (page * a.V + hv) << a.kv.log_ps;  // below 2^31: checked on the host
+      if (ok)
+        for (int h = 0; h < C::kHalves; ++h)
+          tma_load_2d(k_s + st * C::kTileBytes + h * C::kHalfBytes + lane * ps * 128, &kmap, h * 64, row, &B.k_full[st]);
+      issued_k = t + 1;
+      __syncwarp();
+      if (!at_wait(&B.v_empty[st], ph, B, a.status)) live = false;
+      if (!live) break;
+      if (lane == 0) mbar_arrive_expect_tx(&B.v_full[st], (uint32_t)(__popc(good) * ps * D * 2));
+      __syncwarp();
+      if (ok)
+        for (int h = 0; h < C::kHalves; ++h)
+          tma_load_2d(v_s + st * C::kTileBytes + h * C::kHalfBytes + lane * ps * 128, &vmap, h * 64, row, &B.v_full[st]);
+      issued_v = t + 1;
+      __syncwarp();
+    }
+    // every copy issued must land before the CTA exits, also after an abort
+    if (nt > 0 && !mbar_wait(&B.q_full, 0)) set_status(a.status, kStatusTimeout);
+    for (int t = max(0, issued_k - C::kStages); t < issued_k; ++t)
+      if (!mbar_wait(&B.k_full[t % C::kStages], (t / C::kStages) & 1)) set_status(a.status, kStatusTimeout);
+    for (int t = max(0, issued_v - C::kStages); t < issued_v; ++t)
+      if (!mbar_wait(&B.v_full[t % C::kStages], (t / C::kStages) & 1)) set_status(a.status, kStatusTimeout);
+  } else if (warp == 9) {
+    // ---- products: the warp runs the loop on uniform values, one elected lane issues ----
+    const uint32_t idesc_s = umma_idesc_bf16(kTcRows, kTcBK);
+    const uint32_t idesc_o = umma_idesc_bf16(kTcRows, D) | (1u << 16);  // B with N contiguous
+    auto scores = [&](int i, int t) {
+      const uint32_t qa = smem_u32(q_s) + i * C::kTileBytes, ka = smem_u32(k_s) + (t % C::kStages) * C::kTileBytes;
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * C::kHalfBytes + (k & 3) * 32;
+          umma_ss(tbase + C::kS + i * kTcBK, umma_sdesc_sw128(qa + off), umma_sdesc_sw128(ka + off), idesc_s, k != 0);
+        }
+        umma_commit(&B.s_full[i]);
+        if (i == nq - 1) umma_commit(&B.k_empty[t % C::kStages]);
+      }
+      __syncwarp();
+    };
+    if (nt > 0) {
+      at_wait(&B.q_full, 0, B, a.status);
+      at_wait(&B.k_full[0], 0, B, a.status);
+      tc_fence_after();
+      for (int i = 0; i < nq; ++i) scores(i, 0);
+    }
+    for (int t = 0; t < nt; ++t) {
+      const int st = t % C::kStages;
+      const uint32_t ph = (t / C::kStages) & 1;
+      for (int i = 0; i < nq; ++i) {
+        at_wait(&B.p_ready[i], t & 1, B, a.status);
+        if (i == 0) {
+          at_wait(&B.v_full[st], ph, B, a.status);
+          at_wait(&B.v_ready[st], ph, B, a.status);
+        }
+        tc_fence_after();
+        const uint32_t va = smem_u32(v_s) + st * C::kTileBytes;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kTcBK / 16; ++k)
+            umma_ts(tbase + C::kO + i * D, tbase + C::kS + i * kTcBK + k * 8, sdesc_n_sw128(va + k * 2048, C::kHalfBytes),
+                    idesc_o, (t | k) != 0);
+          umma_commit(&B.pv_done[i]);
+          if (i == nq - 1) umma_commit(&B.v_empty[st]);
+        }
+        __syncwarp();
+        if (t + 1 < nt) {
+          if (i == 0) at_wait(&B.k_full[(t + 1) % C::kStages], ((t + 1) / C::kStages) & 1, B, a.status);
+          at_wait(&B.pv_done[i], t & 1, B, a.status);  // S_i(t + 1) goes over P_i(t)
+          tc_fence_after();
+          scores(i, t + 1);
+        }
+      }
+    }
+    if (elect_one()) {
+      umma_commit(&B.done);
+      if (!mbar_wait(&B.done, 0)) set_status(a.status, kStatusTimeout);
+    }
+    __syncwarp();
+  } else if (warp >= 10) {
+    // ---- V rows that must not be multiplied ----
+    for (int t = 0; t < nt; ++t) {
+      const int st = t % C::kStages, j0 = tile_of(tr, t) << kTcLogBK;
+      at_wait(&B.v_full[st], (t / C::kStages) & 1, B, a.status);
+      const TileInfo &in = B.info[t % kTcInfo];
+      if (in.partial) {
+        uint8_t *v = v_s + st * C::kTileBytes;
+        // lane and step pick a row: 32 rows a step and warp, each row by one lane
+        for (int r0 = (warp - 10) * 32; r0 < kTcBK; r0 += 64) {
+          const int r = r0 + lane, j = j0 + r;
+          const bool live = j <= p1 && j < s.n && (a.window <= 0 || p0 - j < a.window || j < a.n_sinks) &&
+                            !(in.bad[r >> 5] >> (r & 31) & 1);
+          bool clear = !live;
+          if (live) {
+            for (int i = 0; i < C::kHalves * 8 && !clear; ++i) {
+              const uint4 x = *reinterpret_cast<const uint4 *>(v + (i >> 3) * C::kHalfBytes + r * 128 +
+                                                               (((i & 7) + r) & 7) * 16);
+              const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                clear |= (e[k] & 0x7f80u) == 0x7f80u || (e[k] & 0x7f800000u) == 0x7f800000u;
+            }
+          }
+          const uint32_t flag = __ballot_sync(0xffffffffu, live && clear);
+          if (lane == 0) B.flagged[st][r0 >> 5] = flag;
+          if (clear)
+            for (int i = 0; i < C::kHalves * 8; ++i)
+              *reinterpret_cast<uint4 *>(v + (i >> 3) * C::kHalfBytes + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&B.v_ready[st]);
+        mbar_arrive(&B.v_empty[st]);
+      }
+    }
+  } else {
+    // ---- softmax of row tile i: one thread a row ----
+    const int i = warp >> 2, row = threadIdx.x & 127;
+    if (i < nq) {
+      const int tok = tok0 + i * w.tokens + row / a.G;
+      const bool alive = row < w.tokens * a.G && tok < s.m;
+      const int pos = alive ? base + tok : -1;
+      const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+      const uint32_t ts = tbase + lanes + C::kS + i * kTcBK, to = tbase + lanes + C::kO + i * D;
+      const float scale = a.scale_log2;
+      float m = -INFINITY, l = 0.f;  // m in units of log2, scaled
+      for (int t = 0; t < nt; ++t) {
+        const int st = t % C::kStages, j0 = tile_of(tr, t) << kTcLogBK;
+        at_wait(&B.s_full[i], t & 1, B, a.status);
+        tc_fence_after();
+        const TileInfo &in = B.info[t % kTcInfo];
+        float x[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * c]));
+        tmem_wait_ld();
+        bool poison = false;
+        if (in.partial) {
+          // the keys of the tile that this row sees: columns up to hi, from lo on or below the sinks
+          const int hi = min(pos, s.n - 1) - j0;
+          const int lo = a.window > 0 ? pos - a.window + 1 - j0 : INT_MIN;
+          const int sk = a.window > 0 ? a.n_sinks - j0 : 0;
+          at_wait(&B.v_ready[st], (t / C::kStages) & 1, B, a.status);
+          const float none = scale < 0.f ? INFINITY : -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 128; ++c) {
+            const bool v = c <= hi && (c >= lo || c < sk) && !(in.bad[c >> 5] >> (c & 31) & 1);
+            if (!v) x[c] = none;
+            poison |= v && (B.flagged[st][c >> 5] >> (c & 31) & 1);
+          }
+        }
+        float mx;
+        if (scale >= 0.f) {
+          float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
+#pragma unroll
+          for (int c = 4; c < 128; c += 4) {
+            m0 = max_nan(m0, x[c]);
+            m1 = max_nan(m1, x[c + 1]);
+            m2 = max_nan(m2, x[c + 2]);
+            m3 = max_nan(m3, x[c + 3]);
+          }
+          mx = max_nan(max_nan(m0, m1), max_nan(m2, m3));
+        } else {
+          mx = x[0];
+#pragma unroll
+          for (int c = 1; c < 128; ++c) mx = min_nan(mx, x[c]);
+        }
+        mx *= scale;  // scale is not 0
+        if (mx == INFINITY) mx = NAN;  // an infinite score that is seen: the whole row is NaN
+        // a row that exceeds its maximum by more than the slack, or has none yet, takes the new one
+        const bool grow = alive && !(mx <= m + kTcLazy);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float nm = grow ? mx : m;
+          const float f = m == -INFINITY ? 0.f : ex2(m - nm);  // l and O are 0 without a maximum
+          if (t > 0) {
+            at_wait(&B.pv_done[i], (t - 1) & 1, B, a.status);
+            tc_fence_after();
+            const float fo = grow ? f : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x16(to + c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * fo);
+              tmem_st_32x32b_x16(to + c, v);
+            }
+            tmem_wait_st();
+          }
+          if (grow) {
+            l *= f;
+            m = nm;
+          }
+        }
+        const float sub = m == -INFINITY ? 0.f : m;
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t p[32];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float y0 = ex2(fmaf(x[c + e], scale, -sub)), y1 = ex2(fmaf(x[c + e + 1], scale, -sub));
+            l0 += y0;
+            l1 += y1;
+            p[e / 2] = pack_bf16x2(y0, y1);
+          }
+          tmem_st_32x32b_x16(ts + c / 2, p);
+        }
+        l += l0 + l1;
+        if (poison) l = NAN;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.p_ready[i]);
+      }
+      // ---- output rows ----
+      if (nt > 0) at_wait(&B.pv_done[i], (nt - 1) & 1, B, a.status);
+      tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.0f / l;
+      uint16_t *dst = a.out + ((size_t)(s.q0 + tok) * a.H + (size_t)hv * a.G + row % a.G) * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t v[32];
+        if (nt > 0) {
+          tmem_ld_32x32b_x32(to + c, v);
+          tmem_wait_ld();
+        }
+        if (alive) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              o[k] = nt > 0 && l != 0.f ? pack_bf16x2(__uint_as_float(v[e + 2 * k]) * inv, __uint_as_float(v[e + 2 * k + 1]) * inv) : 0u;
+            *reinterpret_cast<uint4 *>(dst + c + e) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tbase, C::kTmemCols);
+  }
+}
+
+template <int D>
+cudaError_t launch_tc(const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) {
+  using C = TcCfg<D>;
+  TcArgs w{a, kTcRows / a.G};
+  auto fn = tma_encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const int ps = 1 << a.kv.log_ps;
+  CUtensorMap qm, km, vm;
+  const cuuint32_t one[3] = {1, 1, 1};
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.H, (cuuint64_t)a.T};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.ld_q * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.G, (cuuint32_t)w.tokens};
+    if (fn(&qm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(a.q), dims, strides, box, one,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  const int rows = c.n_pages * a.V * ps;  // below 2^31: checked on the host
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)ps};
+  for (int i = 0; i < 2; ++i)
+    if (fn(i ? &vm : &km, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(i ? a.v : a.k), dims, strides, box,
+           one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  const int pair = 2 * w.tokens;
+  const long long items = a.kv.q_start ? (long long)a.T / pair + std::min(a.T, a.kv.n_seqs)
+                                       : (long long)a.kv.n_seqs * ((a.kv.per + pair - 1) / pair);
+  if (items * a.V > 0x7fffffffll) return cudaErrorInvalidValue;
+  const size_t smem = (size_t)C::kSmemTiles * C::kTileBytes + sizeof(TcBars<D>) + 1024;
+  cudaError_t err = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  attn_tc_kernel<D><<<(unsigned)(items * a.V), kTcThreads, smem, s>>>(qm, km, vm, w);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) {
+  return d.head_dim == 128 ? launch_tc<128>(a, c, s) : launch_tc<64>(a, c, s);
+}
+
+}  // namespace moe
