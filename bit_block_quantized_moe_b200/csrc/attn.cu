@@ -1,12 +1,18 @@
-// Attention over the paged cache, small tiles of queries on the legacy tensor path (mma.sync).
+// Attention of verify windows (1 to 8 new tokens a sequence) over the paged cache, on the legacy tensor path
+// (mma.sync): the work is reading the cache once, and a window's few rows fill 16-row products, not 128-row ones.
 //
 // The query heads of a group share their key/value head, so that a tile's rows are (token, head of the group) pairs:
 // row r is token r / G, head r % G.  One pass over the keys with the running maximum and sum of the softmax:
 //   s_j = scale q.k_j,  m' = max(m, max_j s_j),  l' = l e^(m - m') + sum_j e^(s_j - m'),  o' = o e^(m - m') + ...
-// in base 2 with scale * log2(e) folded in.  A CTA holds WM x WK warps: WM tiles of 16 rows, and each 64-key tile
-// is shared out over WK warps, which keep their own m, l, o and join them at the end.  Keys and values come by
-// cp.async in 64-key stages (rows of the page table looked up per copy, rows that no query of the tile sees filled
-// with zeros, so that nothing behind them can reach an output).
+// in base 2 with scale * log2(e) folded in.
+//
+// Split: all 128-key tiles of all (sequence, key/value head, row tile) groups stand in one line, which is cut into
+// equal shares, one a CTA, whatever the lengths (they are read on the device, so that a captured graph follows them).
+// A CTA's share is one stream of loads through its ring of stages, across group ends.  A group that is cut leaves
+// parts (m, l, o) in the workspace; the CTA that brings the last one joins them in share order, so that the result
+// does not depend on which that is.  In a CTA, WM x WK warps take 16 rows and 1/WK of a tile's keys each and join
+// their m, l, o pairwise at a group's end.  Keys and values come by cp.async; rows that no query of the window sees
+// are filled with zeros, so that nothing behind them can reach an output.
 #include <algorithm>
 
 #include "attn.cuh"
@@ -15,10 +21,8 @@
 namespace moe {
 namespace {
 
-constexpr int kBK = 64;         // keys a stage
-constexpr int kLogBK = 6;
-constexpr int kWinStages = 3;
-constexpr int kWave = 296;      // CTAs aimed at when a window's keys are split: two a SM
+constexpr int kBK = 128;        // keys a tile
+constexpr int kLogBK = 7;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -44,105 +48,199 @@ struct WinCfg {
   static constexpr int kKeys = kBK / WK;            // keys a warp
   static constexpr int kTileBytes = kBK * D * 2;    // K or V of a stage
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kSmem = kWinStages * kStageBytes;
-  static_assert(WK == 1 || WK * kRows * (D + 2) * 4 <= kSmem, "the warps' join reuses the stages");
+  static constexpr int kStages = D == 128 ? 3 : 5;
+  static constexpr int kOut = D / 2;                // accumulators a lane
+  static constexpr int kJoinBytes = WM * (WK / 2) * 32 * (kOut + 4) * 4;
+  static constexpr int kSmem = kStages * kStageBytes + kJoinBytes;
 };
 
 struct WinArgs {
   AttnArgs a;
-  int row_tiles, splits;
+  int row_tiles;
+};
+
+// Where a CTA stands in the line of tiles: tile t of group g (key/value head and row tile) of sequence b.
+struct Cursor {
+  int b, g, t, nt;
+  SeqView s;
+  TileRange r;
+
+  __device__ __forceinline__ void sequence(const AttnArgs &a, int seq) {
+    b = seq;
+    s = seq_view(nullptr, a.kv.kv_len, b, a.kv.per, a.T, a.kv.cap);
+    r = tile_range(s.n - s.m, s.n - 1, s.n, a.window, a.n_sinks, kLogBK);
+    nt = max(r.count, 1);  // an empty sequence has one tile in which nothing is seen
+  }
+  __device__ __forceinline__ void advance(const AttnArgs &a, int groups) {
+    if (++t < nt) return;
+    t = 0;
+    if (++g < groups) return;
+    g = 0;
+    if (b + 1 < a.kv.n_seqs) sequence(a, b + 1);
+  }
+  __device__ __forceinline__ int key0() const { return tile_of(r, t) << kLogBK; }
 };
 
 template <int D, int WM, int WK>
-__global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads) attn_mma_kernel(const __grid_constant__ WinArgs w) {
+__global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads, 1) attn_window_kernel(const __grid_constant__ WinArgs w) {
   using C = WinCfg<D, WM, WK>;
   constexpr int kChunks = D / 8;  // 16-byte pieces a row
   extern __shared__ __align__(128) uint8_t win_smem[];
   __shared__ uint32_t bad_v[kBK / 32];
+  __shared__ long long scan_s[C::kThreads / 32];
+  __shared__ int found_b, last_s;
+  __shared__ long long found_base;
   const AttnArgs &a = w.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int wm = warp % WM, wk = warp / WM;
-  int u = blockIdx.x;
-  const int split = u % w.splits;
-  u /= w.splits;
-  const int rt = u % w.row_tiles;
-  u /= w.row_tiles;
-  const int hv = u % a.V, b = u / a.V;
+  const int groups = a.V * w.row_tiles, rows = a.kv.per * a.G;
 
+  // ---- this CTA's share [x0, x1) of the line, and the sequence in which it begins
   if (blockIdx.x == 0) check_sequences(a.kv, a.T, a.status);
-  const SeqView s = seq_view(a.kv.q_start, a.kv.kv_len, b, a.kv.per, a.T, a.kv.cap);
-  const int rows = s.m * a.G, r0 = rt * C::kRows;
-  if (r0 >= rows) return;
-  const int base = s.n - s.m;  // position of new token 0
-  const int p0 = base + r0 / a.G, p1 = base + (min(rows, r0 + C::kRows) - 1) / a.G;
-  const TileRange tr = tile_range(p0, p1, s.n, a.window, a.n_sinks, kLogBK);
-  const int t_lo = (int)((long long)tr.count * split / w.splits), t_hi = (int)((long long)tr.count * (split + 1) / w.splits);
-  const int32_t *table = a.kv.table + (size_t)b * a.kv.max_pages;
-
-  // the queries of this warp's 16 rows, as A fragments
-  const int ra = r0 + 16 * wm + g, rb = ra + 8;
-  const int pa = ra < rows ? base + ra / a.G : -1, pb = rb < rows ? base + rb / a.G : -1;
-  const uint16_t *qa = a.q + (size_t)(s.q0 + ra / a.G) * a.ld_q + (size_t)(hv * a.G + ra % a.G) * D;
-  const uint16_t *qb = a.q + (size_t)(s.q0 + rb / a.G) * a.ld_q + (size_t)(hv * a.G + rb % a.G) * D;
-  uint32_t qf[D / 16][4];
-#pragma unroll
-  for (int k = 0; k < D / 16; ++k) {
-    qf[k][0] = ra < rows ? __ldg(reinterpret_cast<const uint32_t *>(qa + 16 * k + 2 * c)) : 0u;
-    qf[k][1] = rb < rows ? __ldg(reinterpret_cast<const uint32_t *>(qb + 16 * k + 2 * c)) : 0u;
-    qf[k][2] = ra < rows ? __ldg(reinterpret_cast<const uint32_t *>(qa + 16 * k + 8 + 2 * c)) : 0u;
-    qf[k][3] = rb < rows ? __ldg(reinterpret_cast<const uint32_t *>(qb + 16 * k + 8 + 2 * c)) : 0u;
+  long long total = 0;
+  for (int c0 = 0; c0 < a.kv.n_seqs; c0 += C::kThreads) {
+    const int b = c0 + threadIdx.x;
+    Cursor q;
+    q.nt = 0;
+    if (b < a.kv.n_seqs) q.sequence(a, b);
+    total += q.nt;
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) scan_s[warp] = total;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < C::kThreads / 32; ++i) total += scan_s[i];
+  total *= groups;
+  const int shares = (int)min((long long)gridDim.x, total);
+  if ((int)blockIdx.x >= shares) return;
+  const long long x0 = total * blockIdx.x / shares, x1 = total * (blockIdx.x + 1) / shares;
+  long long base = 0;
+  for (int c0 = 0; c0 < a.kv.n_seqs && base <= x0; c0 += C::kThreads) {
+    const int b = c0 + threadIdx.x;
+    Cursor q;
+    q.nt = 0;
+    if (b < a.kv.n_seqs) q.sequence(a, b);
+    long long incl = q.nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    __syncthreads();
+    if (lane == 31) scan_s[warp] = incl;
+    __syncthreads();
+    long long before = incl - q.nt, sum = 0;
+#pragma unroll
+    for (int i = 0; i < C::kThreads / 32; ++i) {
+      if (i < warp) before += scan_s[i];
+      sum += scan_s[i];
+    }
+    const long long at = base + before * groups;
+    if (q.nt > 0 && at <= x0 && x0 < at + (long long)q.nt * groups) {
+      found_b = b;
+      found_base = at;
+    }
+    base += sum * groups;
+  }
+  __syncthreads();
+  Cursor cur;
+  cur.sequence(a, found_b);
+  cur.g = (int)((x0 - found_base) / cur.nt);
+  cur.t = (int)((x0 - found_base) % cur.nt);
+  Cursor ahead = cur;
 
   const uint32_t smem0 = smem_u32(win_smem);
-  auto load = [&](int t) {
-    if (t < t_hi) {
-      const int j0 = tile_of(tr, t) << kLogBK;
-      const uint32_t st = smem0 + (uint32_t)((t - t_lo) % kWinStages) * C::kStageBytes;
-      for (int i = threadIdx.x; i < kBK * kChunks; i += C::kThreads) {
-        const int r = i / kChunks, ch = i % kChunks, j = j0 + r;
+  long long xl = x0;
+  int ls = 0;  // stage of the next load
+  auto load = [&] {
+    if (xl < x1) {
+      const int j0 = ahead.key0(), p0 = ahead.s.n - ahead.s.m, hv = ahead.g / w.row_tiles;
+      const int32_t *table = a.kv.table + (size_t)ahead.b * a.kv.max_pages;
+      const uint32_t st = smem0 + (uint32_t)ls * C::kStageBytes;
+      constexpr int kPass = C::kThreads / kChunks;  // keys a pass of the CTA
+      const int r0 = threadIdx.x / kChunks, ch = threadIdx.x % kChunks;
+      const size_t head = ((size_t)hv << a.kv.log_ps) * D + (size_t)ch * 8;
+      int64_t row[kBK / kPass];
+#pragma unroll
+      for (int i = 0; i < kBK / kPass; ++i) {
+        const int j = j0 + r0 + i * kPass;
         // seen by the first or the last query that could: the visible set of a query grows at one end and
         // shrinks at the other, so that a key in neither is in none between them
-        bool ok = j <= p1 && j < s.n && (a.window <= 0 || p0 - j < a.window || j < a.n_sinks);
-        int64_t row = -1;
-        if (ok) row = cache_row(table, j, a.kv.log_ps, a.kv.n_pages, a.V);
-        ok = ok && row >= 0;
-        const size_t off = ok ? ((size_t)row + ((size_t)hv << a.kv.log_ps)) * D + (size_t)ch * 8 : 0;
-        const uint32_t dst = st + (uint32_t)(r * kChunks + (ch ^ (r & 7))) * 16u;
-        cp_async16_or_zero(dst, a.k + off, ok);
-        cp_async16_or_zero(dst + C::kTileBytes, a.v + off, ok);
+        const bool ok = j < ahead.s.n && (a.window <= 0 || p0 - j < a.window || j < a.n_sinks);
+        row[i] = ok ? cache_row(table, j, a.kv.log_ps, a.kv.n_pages, a.V) : -1;
       }
+#pragma unroll
+      for (int i = 0; i < kBK / kPass; ++i) {
+        const int r = r0 + i * kPass;
+        const size_t off = row[i] >= 0 ? (size_t)row[i] * D + head : 0;
+        const uint32_t dst = st + (uint32_t)(r * kChunks + (ch ^ (r & 7))) * 16u;
+        cp_async16_or_zero(dst, a.k + off, row[i] >= 0);
+        cp_async16_or_zero(dst + C::kTileBytes, a.v + off, row[i] >= 0);
+      }
+      ahead.advance(a, groups);
+      ++xl;
     }
+    ls = ls + 1 == C::kStages ? 0 : ls + 1;
     cp_async_commit();
   };
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i) load();
 
+  uint32_t qf[D / 16][4];
   float o[D / 8][4];
+  float ma = 0.f, mb = 0.f, la = 0.f, lb = 0.f;
+  int r0 = 0, hv = 0, base_pos = 0, pa = -1, pb = -1, cs = 0;
+  bool fresh = true;
+  for (long long x = x0; x < x1; ++x) {
+    if (fresh) {
+      // the queries of this warp's 16 rows, as A fragments
+      fresh = false;
+      hv = cur.g / w.row_tiles;
+      r0 = (cur.g - hv * w.row_tiles) * C::kRows;
+      base_pos = cur.s.n - cur.s.m;
+      const int ra = r0 + 16 * wm + g, rb = ra + 8;
+      pa = ra < rows ? base_pos + ra / a.G : -1;
+      pb = rb < rows ? base_pos + rb / a.G : -1;
+      const uint16_t *qa = a.q + (size_t)(cur.s.q0 + ra / a.G) * a.ld_q + (size_t)(hv * a.G + ra % a.G) * D;
+      const uint16_t *qb = a.q + (size_t)(cur.s.q0 + rb / a.G) * a.ld_q + (size_t)(hv * a.G + rb % a.G) * D;
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
-
+      for (int k = 0; k < D / 16; ++k) {
+        qf[k][0] = ra < rows ? __ldg(reinterpret_cast<const uint32_t *>(qa + 16 * k + 2 * c)) : 0u;
+        qf[k][1] = rb < rows ? __ldg(reinterpret_cast<const uint32_t *>(qb + 16 * k + 2 * c)) : 0u;
+        qf[k][2] = ra < rows ? __ldg(reinterpret_cast<const uint32_t *>(qa + 16 * k + 8 + 2 * c)) : 0u;
+        qf[k][3] = rb < rows ? __ldg(reinterpret_cast<const uint32_t *>(qb + 16 * k + 8 + 2 * c)) : 0u;
+      }
 #pragma unroll
-  for (int i = 0; i < kWinStages - 1; ++i) load(t_lo + i);
-  for (int t = t_lo; t < t_hi; ++t) {
-    cp_async_wait_group<kWinStages - 2>();
-    __syncthreads();
-    load(t + kWinStages - 1);
-    const int j0 = tile_of(tr, t) << kLogBK;
-    const uint32_t st = smem0 + (uint32_t)((t - t_lo) % kWinStages) * C::kStageBytes;
-    // every key of the tile is seen by every row and lies in a valid page: no masks
-    bool full = tile_full(p0, p1, j0, kBK, s.n, a.window, a.n_sinks);
-    for (int p = j0 >> a.kv.log_ps; full && p <= (j0 + kBK - 1) >> a.kv.log_ps; ++p) {
-      const int32_t page = __ldg(table + p);
-      full = page >= 0 && page < a.kv.n_pages;
+      for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      ma = mb = -INFINITY;
+      la = lb = 0.f;
     }
-    if (!full) {
+    cp_async_wait_group<C::kStages - 2>();
+    __syncthreads();
+    load();
+    const int j0 = cur.key0(), n = cur.s.n;
+    const int32_t *table = a.kv.table + (size_t)cur.b * a.kv.max_pages;
+    const uint32_t st = smem0 + (uint32_t)cs * C::kStageBytes;
+    // every key of the tile is seen by every row and lies in a valid page: no masks
+    bool full = tile_full(base_pos, n - 1, j0, kBK, n, a.window, a.n_sinks);
+    if (full) {
+      const int first = j0 >> a.kv.log_ps, pages = kBK >> a.kv.log_ps;
+      const int32_t page = lane < pages ? __ldg(table + first + lane) : 0;
+      full = __all_sync(0xffffffffu, page >= 0 && page < a.kv.n_pages);
+    }
+    const bool mixed = !full && a.kv.per > 1;
+    if (mixed) {
       // A key that only some of the rows see: 0 * v is NaN when v is not finite, so such rows of V are cleared and
       // the rows that do see them become NaN.
-      uint8_t *vt = win_smem + ((t - t_lo) % kWinStages) * C::kStageBytes + C::kTileBytes;
+      uint8_t *vt = win_smem + cs * C::kStageBytes + C::kTileBytes;
       if (threadIdx.x < kBK / 32) bad_v[threadIdx.x] = 0;
       __syncthreads();
+#pragma unroll 4
       for (int i = threadIdx.x; i < kBK * kChunks; i += C::kThreads) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(vt + (size_t)i * 16);
-        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+        const uint4 v4 = *reinterpret_cast<const uint4 *>(vt + (size_t)i * 16);
+        const uint32_t v[4] = {v4.x, v4.y, v4.z, v4.w};
         bool bad = false;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -153,7 +251,7 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads) attn_mma_kernel(c
         }
       }
       __syncthreads();
-      if (bad_v[0] | bad_v[1]) {
+      if (bad_v[0] | bad_v[1] | bad_v[2] | bad_v[3]) {
         for (int i = threadIdx.x; i < kBK * kChunks; i += C::kThreads) {
           const int r = i / kChunks;
           if (bad_v[r >> 5] >> (r & 31) & 1) *reinterpret_cast<uint4 *>(vt + (size_t)i * 16) = make_uint4(0, 0, 0, 0);
@@ -165,17 +263,17 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads) attn_mma_kernel(c
     float sc[C::kKeys / 8][4];
 #pragma unroll
     for (int i = 0; i < C::kKeys / 8; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
-    const int key0 = wk * C::kKeys;
+    const int k0 = wk * C::kKeys;
 #pragma unroll
-    for (int n = 0; n < C::kKeys / 16; ++n) {
-      const int r = key0 + 16 * n + (lane & 7) + ((lane & 16) ? 8 : 0);
+    for (int i = 0; i < C::kKeys / 16; ++i) {
+      const int r = k0 + 16 * i + (lane & 7) + ((lane & 16) ? 8 : 0);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const int ch = 2 * k + ((lane >> 3) & 1);
         uint32_t b0, b1, b2, b3;
         ldsm_x4(st + (uint32_t)(r * kChunks + (ch ^ (r & 7))) * 16u, b0, b1, b2, b3);
-        mma_bf16_16816(sc[2 * n], qf[k], b0, b1, sc[2 * n]);
-        mma_bf16_16816(sc[2 * n + 1], qf[k], b2, b3, sc[2 * n + 1]);
+        mma_bf16_16816(sc[2 * i], qf[k], b0, b1, sc[2 * i]);
+        mma_bf16_16816(sc[2 * i + 1], qf[k], b2, b3, sc[2 * i + 1]);
       }
     }
 #pragma unroll
@@ -188,15 +286,15 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads) attn_mma_kernel(c
       for (int i = 0; i < C::kKeys / 8; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int jj = key0 + 8 * i + 2 * c + e, j = j0 + jj;
-          const bool in = j < s.n && cache_row(table, j, a.kv.log_ps, a.kv.n_pages, a.V) >= 0;
-          const bool va = in && key_seen(pa, j, s.n, a.window, a.n_sinks);
-          const bool vb = in && key_seen(pb, j, s.n, a.window, a.n_sinks);
-          const bool bad = bad_v[jj >> 5] >> (jj & 31) & 1;
+          const int jj = k0 + 8 * i + 2 * c + e, j = j0 + jj;
+          bool va = key_seen(pa, j, n, a.window, a.n_sinks), vb = key_seen(pb, j, n, a.window, a.n_sinks);
+          if ((va || vb) && cache_row(table, j, a.kv.log_ps, a.kv.n_pages, a.V) < 0) {
+            set_status(a.status, kStatusBadIndex);
+            va = vb = false;
+          }
+          const bool bad = mixed && (bad_v[jj >> 5] >> (jj & 31) & 1);
           nan_a |= bad && va;
           nan_b |= bad && vb;
-          if (j < s.n && !in && (va || vb || key_seen(pa, j, s.n, a.window, a.n_sinks) || key_seen(pb, j, s.n, a.window, a.n_sinks)))
-            set_status(a.status, kStatusBadIndex);
           if (!va) sc[i][e] = -INFINITY;
           if (!vb) sc[i][2 + e] = -INFINITY;
         }
@@ -215,15 +313,15 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads) attn_mma_kernel(c
     const float na = fmaxf(ma, xa), nb = fmaxf(mb, xb);
     // nothing seen yet: subtract 0, so that e^(-inf - 0) = 0
     const float sa = na == -INFINITY ? 0.f : na, sb = nb == -INFINITY ? 0.f : nb;
-    const float fa = exp2f(ma - sa), fb = exp2f(mb - sb);
+    const float fa = ex2(ma - sa), fb = ex2(mb - sb);
     ma = na;
     mb = nb;
     float ta = nan_a ? NAN : 0.f, tb = nan_b ? NAN : 0.f;
     uint32_t pf[C::kKeys / 8][2];
 #pragma unroll
     for (int i = 0; i < C::kKeys / 8; ++i) {
-      const float e0 = exp2f(sc[i][0] - sa), e1 = exp2f(sc[i][1] - sa);
-      const float e2 = exp2f(sc[i][2] - sb), e3 = exp2f(sc[i][3] - sb);
+      const float e0 = ex2(sc[i][0] - sa), e1 = ex2(sc[i][1] - sa);
+      const float e2 = ex2(sc[i][2] - sb), e3 = ex2(sc[i][3] - sb);
       ta += e0 + e1;
       tb += e2 + e3;
       pf[i][0] = pack_bf16x2(e0, e1);
@@ -239,9 +337,9 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads) attn_mma_kernel(c
       o[i][3] *= fb;
     }
 #pragma unroll
-    for (int n = 0; n < C::kKeys / 16; ++n) {
-      const uint32_t af[4] = {pf[2 * n][0], pf[2 * n][1], pf[2 * n + 1][0], pf[2 * n + 1][1]};
-      const int r = key0 + 16 * n + (lane & 15);
+    for (int i = 0; i < C::kKeys / 16; ++i) {
+      const uint32_t af[4] = {pf[2 * i][0], pf[2 * i][1], pf[2 * i + 1][0], pf[2 * i + 1][1]};
+      const int r = k0 + 16 * i + (lane & 15);
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) {
         const int ch = 2 * d + (lane >> 4);
@@ -251,125 +349,147 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads) attn_mma_kernel(c
         mma_bf16_16816(o[2 * d + 1], af, b2, b3, o[2 * d + 1]);
       }
     }
-  }
-  cp_async_wait_all();
-#pragma unroll
-  for (int d = 1; d < 4; d <<= 1) {
-    la += __shfl_xor_sync(0xffffffffu, la, d);
-    lb += __shfl_xor_sync(0xffffffffu, lb, d);
-  }
+    cs = cs + 1 == C::kStages ? 0 : cs + 1;
 
-  // join the WK warps of each row tile: parts to shared memory, summed in warp order
-  float *os = reinterpret_cast<float *>(win_smem);               // [WK][rows][D]
-  float *ms = os + (size_t)WK * C::kRows * D;                    // [WK][rows] maximum, then sum
-  __syncthreads();
-  const int rl = wk * C::kRows + 16 * wm + g;
+    if (cur.t + 1 == cur.nt || x + 1 == x1) {
+      // ---- the end of this CTA's part of the group: join the WK warps of each row tile pairwise
+      fresh = true;
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    *reinterpret_cast<float2 *>(os + (size_t)rl * D + 8 * i + 2 * c) = make_float2(o[i][0], o[i][1]);
-    *reinterpret_cast<float2 *>(os + (size_t)(rl + 8) * D + 8 * i + 2 * c) = make_float2(o[i][2], o[i][3]);
-  }
-  if (c == 0) {
-    ms[2 * rl] = ma;
-    ms[2 * rl + 1] = la;
-    ms[2 * (rl + 8)] = mb;
-    ms[2 * (rl + 8) + 1] = lb;
-  }
-  __syncthreads();
-  float *po = a.part + (size_t)blockIdx.x * C::kRows * (D + 2), *pm = po + (size_t)C::kRows * D;
-  for (int i = threadIdx.x; i < C::kRows * (D / 2); i += C::kThreads) {
-    const int r = i / (D / 2), d = 2 * (i % (D / 2)), rg = r0 + r;
-    if (rg >= rows) continue;
-    float m = -INFINITY, l = 0.f, x = 0.f, y = 0.f;
-    for (int k = 0; k < WK; ++k) m = fmaxf(m, ms[2 * (k * C::kRows + r)]);
-    const float sub = m == -INFINITY ? 0.f : m;
-    for (int k = 0; k < WK; ++k) {
-      const float f = exp2f(ms[2 * (k * C::kRows + r)] - sub);
-      const float2 v = *reinterpret_cast<const float2 *>(os + (size_t)(k * C::kRows + r) * D + d);
-      l += f * ms[2 * (k * C::kRows + r) + 1];
-      x += f * v.x;
-      y += f * v.y;
-    }
-    if (w.splits == 1) {
-      const float inv = l == 0.f ? 0.f : 1.0f / l;
-      uint16_t *dst = a.out + ((size_t)(s.q0 + rg / a.G) * a.H + (size_t)hv * a.G + rg % a.G) * D + d;
-      *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(x * inv, y * inv);
-    } else {
-      *reinterpret_cast<float2 *>(po + (size_t)r * D + d) = make_float2(x, y);
-      if (d == 0) {
-        pm[2 * r] = m;
-        pm[2 * r + 1] = l;
+      for (int d = 1; d < 4; d <<= 1) {
+        la += __shfl_xor_sync(0xffffffffu, la, d);
+        lb += __shfl_xor_sync(0xffffffffu, lb, d);
+      }
+      float *join = reinterpret_cast<float *>(win_smem + C::kStages * C::kStageBytes);
+#pragma unroll
+      for (int h = WK / 2; h > 0; h >>= 1) {
+        if (wk >= h && wk < 2 * h) {
+          float *q = join + (size_t)((wk - h) * WM + wm) * 32 * (C::kOut + 4) + lane;
+#pragma unroll
+          for (int i = 0; i < C::kOut; ++i) q[32 * i] = o[i >> 2][i & 3];
+          q[32 * C::kOut] = ma;
+          q[32 * (C::kOut + 1)] = mb;
+          q[32 * (C::kOut + 2)] = la;
+          q[32 * (C::kOut + 3)] = lb;
+        }
+        __syncthreads();
+        if (wk < h) {
+          const float *q = join + (size_t)(wk * WM + wm) * 32 * (C::kOut + 4) + lane;
+          const float m2a = q[32 * C::kOut], m2b = q[32 * (C::kOut + 1)];
+          const float ja = fmaxf(ma, m2a), jb = fmaxf(mb, m2b);
+          const float ua = ja == -INFINITY ? 0.f : ja, ub = jb == -INFINITY ? 0.f : jb;
+          const float f0 = ex2(ma - ua), f1 = ex2(m2a - ua), f2 = ex2(mb - ub), f3 = ex2(m2b - ub);
+          ma = ja;
+          mb = jb;
+          la = la * f0 + q[32 * (C::kOut + 2)] * f1;
+          lb = lb * f2 + q[32 * (C::kOut + 3)] * f3;
+#pragma unroll
+          for (int i = 0; i < C::kOut; ++i) {
+            const float v = q[32 * i];
+            o[i >> 2][i & 3] = (i & 2) ? o[i >> 2][i & 3] * f2 + v * f3 : o[i >> 2][i & 3] * f0 + v * f1;
+          }
+        }
+        __syncthreads();
+      }
+      const long long gs = x - cur.t, ge = gs + cur.nt;
+      const bool whole = gs >= x0 && ge <= x1;
+      const int ra = 16 * wm + g, live = min(rows - r0, C::kRows);
+      if (whole) {
+        if (wk == 0) {
+          const float ia = la == 0.f ? 0.f : 1.0f / la, ib = lb == 0.f ? 0.f : 1.0f / lb;
+          const int qa = r0 + ra, qb = qa + 8;
+          uint16_t *da = a.out + ((size_t)(cur.s.q0 + qa / a.G) * a.H + (size_t)hv * a.G + qa % a.G) * D + 2 * c;
+          uint16_t *db = a.out + ((size_t)(cur.s.q0 + qb / a.G) * a.H + (size_t)hv * a.G + qb % a.G) * D + 2 * c;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            if (ra < live) *reinterpret_cast<uint32_t *>(da + 8 * i) = pack_bf16x2(o[i][0] * ia, o[i][1] * ia);
+            if (ra + 8 < live) *reinterpret_cast<uint32_t *>(db + 8 * i) = pack_bf16x2(o[i][2] * ib, o[i][3] * ib);
+          }
+        }
+      } else {
+        // parts: slot 0 of a share for the group that it begins with, slot 1 for the one that it ends with
+        constexpr size_t kPart = (size_t)C::kRows * (D + 2);
+        float *po = a.part + ((size_t)blockIdx.x * 2 + (gs > x0)) * kPart, *pm = po + (size_t)C::kRows * D;
+        if (wk == 0) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            if (ra < live) __stcg(reinterpret_cast<float2 *>(po + (size_t)ra * D + 8 * i + 2 * c), make_float2(o[i][0], o[i][1]));
+            if (ra + 8 < live)
+              __stcg(reinterpret_cast<float2 *>(po + (size_t)(ra + 8) * D + 8 * i + 2 * c), make_float2(o[i][2], o[i][3]));
+          }
+          if (c == 0) {
+            if (ra < live) __stcg(reinterpret_cast<float2 *>(pm + 2 * ra), make_float2(ma, la));
+            if (ra + 8 < live) __stcg(reinterpret_cast<float2 *>(pm + 2 * (ra + 8)), make_float2(mb, lb));
+          }
+          __threadfence();
+        }
+        // the shares that hold this group; each share is the first of at most one cut group, whose count it keeps
+        const int c0 = (int)(((gs + 1) * shares - 1) / total), c1 = (int)((ge * shares - 1) / total);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          __threadfence();
+          const uint32_t before = atomicAdd(a.counts + c0, 1u);
+          last_s = before == (uint32_t)(c1 - c0);
+          if (last_s) a.counts[c0] = 0;  // for the next call
+          __threadfence();
+        }
+        __syncthreads();
+        if (last_s) {
+          const bool late = gs > total * c0 / shares;  // the first part lies in slot 1
+          for (int i = threadIdx.x; i < live * (D / 2); i += C::kThreads) {
+            const int r = i / (D / 2), d = 2 * (i % (D / 2));
+            float m = -INFINITY, l = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll 8
+            for (int k = c0; k <= c1; ++k) {
+              const float *pk = a.part + ((size_t)k * 2 + (k == c0 && late)) * kPart;
+              const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pk + (size_t)C::kRows * D + 2 * r));
+              const float2 v = __ldcg(reinterpret_cast<const float2 *>(pk + (size_t)r * D + d));
+              const float nm = fmaxf(m, ml.x), u = nm == -INFINITY ? 0.f : nm;
+              const float f0 = ex2(m - u), f1 = ex2(ml.x - u);
+              m = nm;
+              l = l * f0 + ml.y * f1;
+              y0 = y0 * f0 + v.x * f1;
+              y1 = y1 * f0 + v.y * f1;
+            }
+            const float inv = l == 0.f ? 0.f : 1.0f / l;
+            const int rg = r0 + r;
+            uint16_t *dst = a.out + ((size_t)(cur.s.q0 + rg / a.G) * a.H + (size_t)hv * a.G + rg % a.G) * D + d;
+            *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(y0 * inv, y1 * inv);
+          }
+        }
+        __syncthreads();
       }
     }
+    cur.advance(a, groups);
   }
-}
-
-// The parts of each row in split order: one CTA a (sequence, key/value head, row tile).
-template <int D, int ROWS>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ WinArgs w) {
-  const AttnArgs &a = w.a;
-  int u = blockIdx.x;
-  const int rt = u % w.row_tiles;
-  u /= w.row_tiles;
-  const int hv = u % a.V, b = u / a.V;
-  const SeqView s = seq_view(a.kv.q_start, a.kv.kv_len, b, a.kv.per, a.T, a.kv.cap);
-  const int rows = s.m * a.G, r0 = rt * ROWS;
-  for (int i = threadIdx.x; i < ROWS * (D / 2); i += blockDim.x) {
-    const int r = i / (D / 2), d = 2 * (i % (D / 2)), rg = r0 + r;
-    if (rg >= rows) continue;
-    const float *p = a.part + (size_t)blockIdx.x * w.splits * ROWS * (D + 2);
-    float m = -INFINITY, l = 0.f, x = 0.f, y = 0.f;
-    for (int k = 0; k < w.splits; ++k) m = fmaxf(m, p[(size_t)k * ROWS * (D + 2) + ROWS * D + 2 * r]);
-    const float sub = m == -INFINITY ? 0.f : m;
-    for (int k = 0; k < w.splits; ++k) {
-      const float *pk = p + (size_t)k * ROWS * (D + 2);
-      const float f = exp2f(pk[ROWS * D + 2 * r] - sub);
-      const float2 v = *reinterpret_cast<const float2 *>(pk + (size_t)r * D + d);
-      l += f * pk[ROWS * D + 2 * r + 1];
-      x += f * v.x;
-      y += f * v.y;
-    }
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-    uint16_t *dst = a.out + ((size_t)(s.q0 + rg / a.G) * a.H + (size_t)hv * a.G + rg % a.G) * D + d;
-    *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(x * inv, y * inv);
-  }
+  cp_async_wait_all();
 }
 
 template <int D, int WM, int WK>
-cudaError_t launch(WinArgs w, bool window, cudaStream_t s) {
+cudaError_t launch(WinArgs w, cudaStream_t s) {
   using C = WinCfg<D, WM, WK>;
-  const int per = w.a.kv.q_start ? w.a.T : w.a.kv.per;
-  w.row_tiles = (int)(((long long)per * w.a.G + C::kRows - 1) / C::kRows);
-  const long long units = (long long)w.a.kv.n_seqs * w.a.V * w.row_tiles;
-  w.splits = window ? (int)std::max(1ll, kWave / units) : 1;
-  if (units * w.splits > 0x7fffffffll) return cudaErrorInvalidValue;
-  cudaError_t err = cudaFuncSetAttribute(attn_mma_kernel<D, WM, WK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  w.row_tiles = (w.a.kv.per * w.a.G + C::kRows - 1) / C::kRows;
+  cudaError_t err =
+      cudaFuncSetAttribute(attn_window_kernel<D, WM, WK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (err != cudaSuccess) return err;
-  attn_mma_kernel<D, WM, WK><<<(unsigned)(units * w.splits), C::kThreads, C::kSmem, s>>>(w);
-  err = cudaGetLastError();
-  if (err == cudaSuccess && w.splits > 1) {
-    attn_join_kernel<D, C::kRows><<<(unsigned)units, 256, 0, s>>>(w);
-    err = cudaGetLastError();
-  }
-  return err;
+  attn_window_kernel<D, WM, WK><<<kAttnShares, C::kThreads, C::kSmem, s>>>(w);
+  return cudaGetLastError();
 }
 
+// Rows of a window: one, two or four 16-row tiles side by side; more rows than 64 walk the keys again.
 template <int D>
 cudaError_t launch_d(const WinArgs &w, cudaStream_t s) {
-  const bool window = !w.a.kv.q_start && w.a.kv.per <= 8;
   const int rows = w.a.kv.per * w.a.G;
-  if (window && rows <= 16) return launch<D, 1, 4>(w, true, s);
-  if (window && rows <= 32) return launch<D, 2, 2>(w, true, s);
-  return launch<D, 4, 1>(w, window, s);
+  if (rows <= 16) return launch<D, 1, 8>(w, s);
+  if (rows <= 32) return launch<D, 2, 4>(w, s);
+  return launch<D, 4, 2>(w, s);
 }
 
 }  // namespace
 
-// Parts exist only where a window is split, in at most kWave CTAs of at most 64 rows.
-size_t attn_part_bytes(const moe_attn_dims &d, int, int) { return (size_t)kWave * 64 * (d.head_dim + 2) * 4; }
+size_t attn_part_bytes(const moe_attn_dims &d, int, int) { return (size_t)kAttnShares * 2 * 64 * (d.head_dim + 2) * 4; }
 
 cudaError_t launch_attn(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) {
-  WinArgs w{a, 1, 1};
+  WinArgs w{a, 1};
   trace_mark(MOE_KERNEL_ATTN, false, s);
   const bool window = !a.kv.q_start && a.kv.per <= 8;
   const cudaError_t err = !window             ? launch_attn_tc(d, a, c, s)

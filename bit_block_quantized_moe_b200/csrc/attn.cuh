@@ -20,6 +20,8 @@ cudaError_t launch_qk_norm_rope(const moe_attn_dims &d, const uint16_t *qkv, int
                                 const float *gk, float eps, const moe_rope *rope, const moe_kv_cache &c,
                                 const KvArgs &kv, int T, uint16_t *q_out, uint32_t *status, cudaStream_t s);
 
+constexpr int kAttnShares = 148;  // CTAs among which a window call's key tiles are cut, one a SM
+
 struct AttnArgs {
   const uint16_t *q;
   int64_t ld_q;
@@ -30,7 +32,8 @@ struct AttnArgs {
   int window, n_sinks;
   uint16_t *out;
   uint32_t *status;
-  float *part;  // workspace: parts of split sequences
+  float *part;        // workspace: parts of split groups
+  uint32_t *counts;   // workspace header: parts that have come, zero between calls [kAttnShares]
 };
 
 size_t attn_part_bytes(const moe_attn_dims &d, int n_seqs, int T);
@@ -45,6 +48,12 @@ __device__ __forceinline__ void unpack8(const uint4 &r, float (&x)[8]) {
     x[2 * i] = __uint_as_float(w[i] << 16);
     x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {

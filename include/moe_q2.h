@@ -287,10 +287,12 @@ moe_status moe_rmsnorm_residual(float *resid, const uint16_t *y, uint16_t *x_nor
  *   moe_attn_forward    o = attention of q over the cache
  *   moe_linear          resid += o Wo^T
  *   moe_rmsnorm_residual(resid, NULL, x_norm), then the MoE half.
- * Calls are asynchronous, allocate nothing, and take a workspace whose first 256
- * bytes follow the rules of moe_workspace_bytes (sticky status word, zeroed once
- * after allocation and again after MOE_ERR_TIMEOUT; not shared by calls that can
- * run at the same time; read with moe_check_status). */
+ * Calls are asynchronous, allocate nothing, and take a workspace.  Its first 1024
+ * bytes hold the sticky status word (read with moe_check_status) and counters that
+ * every call leaves at zero: zero the workspace (or at least those 1024 bytes) once
+ * after allocating it, and again after a call reported MOE_ERR_TIMEOUT.  One
+ * workspace must not be used by two calls that can run at the same time, two
+ * captured graphs among them. */
 
 /* Matrix product with its epilogue: z = x w^T + bias (exact bf16 products, fp32
  * sums), a = act(z), then
