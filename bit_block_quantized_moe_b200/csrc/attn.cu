@@ -10,13 +10,16 @@
 // equal shares, one a CTA, whatever the lengths (they are read on the device, so that a captured graph follows them).
 // A CTA's share is one stream of loads through its ring of stages, across group ends.  A group that is cut leaves
 // parts (m, l, o) in the workspace; the CTA that brings the last one joins them in share order, so that the result
-// does not depend on which that is.  In a CTA, WM x WK warps take 16 rows and 1/WK of a tile's keys each and join
-// their m, l, o pairwise at a group's end.  Keys and values come by cp.async; rows that no query of the window sees
-// are filled with zeros, so that nothing behind them can reach an output.
+// does not depend on which that is.
+//   last warp        : TMA of K and V, a page at a time, into the ring; 128-byte swizzle;
+//   WM x WK warps    : 16 rows and 1/WK of a tile's keys each, with m, l, o of their own, no waits on one another
+//                      but at a group's end, where they join pairwise.
+// Rows of V that no query of the window sees are masked in the registers that feed the product, so that nothing behind
+// them can reach an output.  Every wait is bounded (sync.cuh).
 #include <algorithm>
 
 #include "attn.cuh"
-#include "sync.cuh"
+#include "tc.cuh"
 
 namespace moe {
 namespace {
@@ -36,14 +39,10 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t &a, uint32_t &
                : "r"(addr)
                : "memory");
 }
-// 16 bytes to shared memory, zeros when !ok.
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-
 template <int D, int WM, int WK>
 struct WinCfg {
-  static constexpr int kThreads = WM * WK * 32;
+  static constexpr int kWarps = WM * WK;            // beside the producer
+  static constexpr int kThreads = (kWarps + 1) * 32;
   static constexpr int kRows = 16 * WM;
   static constexpr int kKeys = kBK / WK;            // keys a warp
   static constexpr int kTileBytes = kBK * D * 2;    // K or V of a stage
@@ -51,7 +50,16 @@ struct WinCfg {
   static constexpr int kStages = D == 128 ? 3 : 5;
   static constexpr int kOut = D / 2;                // accumulators a lane
   static constexpr int kJoinBytes = WM * (WK / 2) * 32 * (kOut + 4) * 4;
+  static constexpr int kHalfBytes = kBK * 128;      // 64 columns of a tile, one swizzle row a key
   static constexpr int kSmem = kStages * kStageBytes + kJoinBytes;
+};
+
+template <int STAGES>
+struct WinBars {
+  uint64_t full[STAGES], empty[STAGES];
+  int partial[STAGES];       // some row does not see some key of the tile
+  uint32_t bad[STAGES][4];   // keys whose page is outside the cache
+  int abort;
 };
 
 struct WinArgs {
@@ -81,12 +89,34 @@ struct Cursor {
   __device__ __forceinline__ int key0() const { return tile_of(r, t) << kLogBK; }
 };
 
+template <class Bars>
+__device__ __forceinline__ bool win_wait(uint64_t *bar, uint32_t parity, Bars &B, uint32_t *status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  if (*reinterpret_cast<volatile int *>(&B.abort)) return false;
+  if (!mbar_wait(bar, parity)) {
+    set_status(status, kStatusTimeout);
+    B.abort = 1;
+    return false;
+  }
+  return true;
+}
+
+// Whether 16 bytes hold a bf16 infinity or NaN.
+__device__ __forceinline__ bool not_finite8(const uint4 &x) {
+  const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) bad |= (e[k] & 0x7f80u) == 0x7f80u || (e[k] & 0x7f800000u) == 0x7f800000u;
+  return bad;
+}
+
 template <int D, int WM, int WK>
-__global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads, 1) attn_window_kernel(const __grid_constant__ WinArgs w) {
+__global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads, 1)
+    attn_window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                       const __grid_constant__ WinArgs w) {
   using C = WinCfg<D, WM, WK>;
-  constexpr int kChunks = D / 8;  // 16-byte pieces a row
-  extern __shared__ __align__(128) uint8_t win_smem[];
-  __shared__ uint32_t bad_v[kBK / 32];
+  extern __shared__ __align__(1024) uint8_t win_smem[];
+  __shared__ WinBars<C::kStages> B;
   __shared__ long long scan_s[C::kThreads / 32];
   __shared__ int found_b, last_s;
   __shared__ long long found_base;
@@ -94,6 +124,14 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads, 1) attn_window_ke
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int wm = warp % WM, wk = warp / WM;
   const int groups = a.V * w.row_tiles, rows = a.kv.per * a.G;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&B.full[i], 1);
+      mbar_init(&B.empty[i], C::kWarps);
+    }
+    B.abort = 0;
+    mbar_fence_init();
+  }
 
   // ---- this CTA's share [x0, x1) of the line, and the sequence in which it begins
   if (blockIdx.x == 0) check_sequences(a.kv, a.T, a.status);
@@ -149,45 +187,58 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads, 1) attn_window_ke
   cur.sequence(a, found_b);
   cur.g = (int)((x0 - found_base) / cur.nt);
   cur.t = (int)((x0 - found_base) % cur.nt);
-  Cursor ahead = cur;
 
-  const uint32_t smem0 = smem_u32(win_smem);
-  long long xl = x0;
-  int ls = 0;  // stage of the next load
-  auto load = [&] {
-    if (xl < x1) {
-      const int j0 = ahead.key0(), p0 = ahead.s.n - ahead.s.m, hv = ahead.g / w.row_tiles;
-      const int32_t *table = a.kv.table + (size_t)ahead.b * a.kv.max_pages;
-      const uint32_t st = smem0 + (uint32_t)ls * C::kStageBytes;
-      constexpr int kPass = C::kThreads / kChunks;  // keys a pass of the CTA
-      const int r0 = threadIdx.x / kChunks, ch = threadIdx.x % kChunks;
-      const size_t head = ((size_t)hv << a.kv.log_ps) * D + (size_t)ch * 8;
-      int64_t row[kBK / kPass];
-#pragma unroll
-      for (int i = 0; i < kBK / kPass; ++i) {
-        const int j = j0 + r0 + i * kPass;
-        // seen by the first or the last query that could: the visible set of a query grows at one end and
-        // shrinks at the other, so that a key in neither is in none between them
-        const bool ok = j < ahead.s.n && (a.window <= 0 || p0 - j < a.window || j < a.n_sinks);
-        row[i] = ok ? cache_row(table, j, a.kv.log_ps, a.kv.n_pages, a.V) : -1;
+  if (warp == C::kWarps) {
+    // ---- producer: lane l < pages has page l of a tile ----
+    const int ps = 1 << a.kv.log_ps, pages = kBK >> a.kv.log_ps;
+    int st = 0;
+    uint32_t ph = 1;
+    long long issued = 0;
+    for (long long x = x0; x < x1; ++x) {
+      const int j0 = cur.key0(), n = cur.s.n, p0 = n - cur.s.m, hv = cur.g / w.row_tiles;
+      const int a0 = j0 + (lane << a.kv.log_ps), e0 = a0 + ps;
+      const bool seen = lane < pages && a0 < n && (a.window <= 0 || e0 - 1 > p0 - a.window || a0 < a.n_sinks);
+      const int page = seen ? __ldg(a.kv.table + (size_t)cur.b * a.kv.max_pages + (a0 >> a.kv.log_ps)) : 0;
+      const bool ok = seen && page >= 0 && page < a.kv.n_pages;
+      const uint32_t good = __ballot_sync(0xffffffffu, ok), wrong = __ballot_sync(0xffffffffu, seen && !ok);
+      if (!__all_sync(0xffffffffu, win_wait(&B.empty[st], ph, B, a.status))) break;
+      if (lane == 0) {
+        B.partial[st] = wrong || !tile_full(p0, n - 1, j0, kBK, n, a.window, a.n_sinks);
+        B.bad[st][0] = B.bad[st][1] = B.bad[st][2] = B.bad[st][3] = 0;
+        if (wrong) {
+          for (int k = 0; k < kBK; ++k)
+            if (wrong >> (k >> a.kv.log_ps) & 1) B.bad[st][k >> 5] |= 1u << (k & 31);
+          set_status(a.status, kStatusBadIndex);
+        }
+        mbar_arrive_expect_tx(&B.full[st], (uint32_t)(__popc(good) * ps * D * 4));
       }
+      __syncwarp();
+      if (ok) {
+        const int row = (page * a.V + hv) << a.kv.log_ps;  // below 2^31: checked on the host
+        uint8_t *dst = win_smem + st * C::kStageBytes + lane * ps * 128;
 #pragma unroll
-      for (int i = 0; i < kBK / kPass; ++i) {
-        const int r = r0 + i * kPass;
-        const size_t off = row[i] >= 0 ? (size_t)row[i] * D + head : 0;
-        const uint32_t dst = st + (uint32_t)(r * kChunks + (ch ^ (r & 7))) * 16u;
-        cp_async16_or_zero(dst, a.k + off, row[i] >= 0);
-        cp_async16_or_zero(dst + C::kTileBytes, a.v + off, row[i] >= 0);
+        for (int h = 0; h < D / 64; ++h) {
+          tma_load_2d(dst + h * C::kHalfBytes, &kmap, h * 64, row, &B.full[st]);
+          tma_load_2d(dst + C::kTileBytes + h * C::kHalfBytes, &vmap, h * 64, row, &B.full[st]);
+        }
       }
-      ahead.advance(a, groups);
-      ++xl;
+      __syncwarp();
+      ++issued;
+      if (++st == C::kStages) {
+        st = 0;
+        ph ^= 1;
+      }
+      cur.advance(a, groups);
     }
-    ls = ls + 1 == C::kStages ? 0 : ls + 1;
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < C::kStages - 1; ++i) load();
+    // every copy issued must land before the CTA exits, also after an abort
+    for (long long t = issued > C::kStages ? issued - C::kStages : 0; t < issued; ++t)
+      if (!mbar_wait(&B.full[t % C::kStages], (uint32_t)(t / C::kStages) & 1)) set_status(a.status, kStatusTimeout);
+    return;
+  }
 
+  // ---- the other warps ----
+  const uint32_t smem0 = smem_u32(win_smem);
+  uint32_t phase = 0;
   uint32_t qf[D / 16][4];
   float o[D / 8][4];
   float ma = 0.f, mb = 0.f, la = 0.f, lb = 0.f;
@@ -217,53 +268,37 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads, 1) attn_window_ke
       ma = mb = -INFINITY;
       la = lb = 0.f;
     }
-    cp_async_wait_group<C::kStages - 2>();
-    __syncthreads();
-    load();
-    const int j0 = cur.key0(), n = cur.s.n;
-    const int32_t *table = a.kv.table + (size_t)cur.b * a.kv.max_pages;
+    const int j0 = cur.key0(), n = cur.s.n, k0 = wk * C::kKeys;
     const uint32_t st = smem0 + (uint32_t)cs * C::kStageBytes;
-    // every key of the tile is seen by every row and lies in a valid page: no masks
-    bool full = tile_full(base_pos, n - 1, j0, kBK, n, a.window, a.n_sinks);
-    if (full) {
-      const int first = j0 >> a.kv.log_ps, pages = kBK >> a.kv.log_ps;
-      const int32_t page = lane < pages ? __ldg(table + first + lane) : 0;
-      full = __all_sync(0xffffffffu, page >= 0 && page < a.kv.n_pages);
-    }
-    const bool mixed = !full && a.kv.per > 1;
-    if (mixed) {
-      // A key that only some of the rows see: 0 * v is NaN when v is not finite, so such rows of V are cleared and
-      // the rows that do see them become NaN.
-      uint8_t *vt = win_smem + cs * C::kStageBytes + C::kTileBytes;
-      if (threadIdx.x < kBK / 32) bad_v[threadIdx.x] = 0;
-      __syncthreads();
-#pragma unroll 4
-      for (int i = threadIdx.x; i < kBK * kChunks; i += C::kThreads) {
-        const uint4 v4 = *reinterpret_cast<const uint4 *>(vt + (size_t)i * 16);
-        const uint32_t v[4] = {v4.x, v4.y, v4.z, v4.w};
-        bool bad = false;
+    win_wait(&B.full[cs], phase, B, a.status);
+    const bool partial = B.partial[cs];
+    // the warp's keys that some row sees and whose values are finite (bit i: key k0 + i), and those seen but not finite
+    unsigned long long use = ~0ull, flagged = 0;
+    if (partial) {
+      use = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          bad |= (v[e] & 0x7f80u) == 0x7f80u || (v[e] & 0x7f800000u) == 0x7f800000u;
-        if (bad) {
-          const int r = i / kChunks;
-          atomicOr(&bad_v[r >> 5], 1u << (r & 31));
+      for (int h = 0; h < C::kKeys; h += 32) {
+        const int kk = k0 + h + (lane & (C::kKeys < 32 ? C::kKeys - 1 : 31)), j = j0 + kk;
+        const bool live = j < n && (a.window <= 0 || base_pos - j < a.window || j < a.n_sinks) &&
+                          !(B.bad[cs][kk >> 5] >> (kk & 31) & 1);
+        bool bad = false;
+        // 0 * v is NaN when v is not finite: where rows differ in what they see, such a key is left out of the
+        // product, and the rows that see it become NaN
+        if (live && a.kv.per > 1) {
+          const uint8_t *v = win_smem + cs * C::kStageBytes + C::kTileBytes + kk * 128;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            bad |= not_finite8(*reinterpret_cast<const uint4 *>(v + (i >> 3) * C::kHalfBytes + (((i & 7) + lane) & 7) * 16));
         }
-      }
-      __syncthreads();
-      if (bad_v[0] | bad_v[1] | bad_v[2] | bad_v[3]) {
-        for (int i = threadIdx.x; i < kBK * kChunks; i += C::kThreads) {
-          const int r = i / kChunks;
-          if (bad_v[r >> 5] >> (r & 31) & 1) *reinterpret_cast<uint4 *>(vt + (size_t)i * 16) = make_uint4(0, 0, 0, 0);
-        }
-        __syncthreads();
+        const unsigned long long lv = __ballot_sync(0xffffffffu, live && !bad), bd = __ballot_sync(0xffffffffu, live && bad);
+        use |= lv << h;
+        flagged |= bd << h;
       }
     }
 
     float sc[C::kKeys / 8][4];
 #pragma unroll
     for (int i = 0; i < C::kKeys / 8; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
-    const int k0 = wk * C::kKeys;
 #pragma unroll
     for (int i = 0; i < C::kKeys / 16; ++i) {
       const int r = k0 + 16 * i + (lane & 7) + ((lane & 16) ? 8 : 0);
@@ -271,7 +306,7 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads, 1) attn_window_ke
       for (int k = 0; k < D / 16; ++k) {
         const int ch = 2 * k + ((lane >> 3) & 1);
         uint32_t b0, b1, b2, b3;
-        ldsm_x4(st + (uint32_t)(r * kChunks + (ch ^ (r & 7))) * 16u, b0, b1, b2, b3);
+        ldsm_x4(st + (uint32_t)((ch >> 3) * C::kHalfBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4)), b0, b1, b2, b3);
         mma_bf16_16816(sc[2 * i], qf[k], b0, b1, sc[2 * i]);
         mma_bf16_16816(sc[2 * i + 1], qf[k], b2, b3, sc[2 * i + 1]);
       }
@@ -281,18 +316,14 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads, 1) attn_window_ke
 #pragma unroll
       for (int e = 0; e < 4; ++e) sc[i][e] *= a.scale_log2;
     bool nan_a = false, nan_b = false;
-    if (!full) {
+    if (partial) {
 #pragma unroll
       for (int i = 0; i < C::kKeys / 8; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int jj = k0 + 8 * i + 2 * c + e, j = j0 + jj;
-          bool va = key_seen(pa, j, n, a.window, a.n_sinks), vb = key_seen(pb, j, n, a.window, a.n_sinks);
-          if ((va || vb) && cache_row(table, j, a.kv.log_ps, a.kv.n_pages, a.V) < 0) {
-            set_status(a.status, kStatusBadIndex);
-            va = vb = false;
-          }
-          const bool bad = mixed && (bad_v[jj >> 5] >> (jj & 31) & 1);
+          const int kk = 8 * i + 2 * c + e, j = j0 + k0 + kk;
+          const bool in = (use | flagged) >> kk & 1, bad = flagged >> kk & 1;
+          const bool va = in && key_seen(pa, j, n, a.window, a.n_sinks), vb = in && key_seen(pb, j, n, a.window, a.n_sinks);
           nan_a |= bad && va;
           nan_b |= bad && vb;
           if (!va) sc[i][e] = -INFINITY;
@@ -340,16 +371,32 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads, 1) attn_window_ke
     for (int i = 0; i < C::kKeys / 16; ++i) {
       const uint32_t af[4] = {pf[2 * i][0], pf[2 * i][1], pf[2 * i + 1][0], pf[2 * i + 1][1]};
       const int r = k0 + 16 * i + (lane & 15);
+      // this lane's keys of the two halves of the fragment: 2c, 2c + 1 and 8 more
+      const uint32_t u = (uint32_t)(use >> (16 * i + 2 * c));
+      const uint32_t v0 = (u & 1 ? 0xffffu : 0u) | (u & 2 ? 0xffff0000u : 0u);
+      const uint32_t v1 = (u & 256 ? 0xffffu : 0u) | (u & 512 ? 0xffff0000u : 0u);
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) {
         const int ch = 2 * d + (lane >> 4);
         uint32_t b0, b1, b2, b3;
-        ldsm_x4_t(st + C::kTileBytes + (uint32_t)(r * kChunks + (ch ^ (r & 7))) * 16u, b0, b1, b2, b3);
+        ldsm_x4_t(st + (uint32_t)(C::kTileBytes + (ch >> 3) * C::kHalfBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4)), b0,
+                  b1, b2, b3);
+        if (partial) {
+          b0 &= v0;
+          b1 &= v1;
+          b2 &= v0;
+          b3 &= v1;
+        }
         mma_bf16_16816(o[2 * d], af, b0, b1, o[2 * d]);
         mma_bf16_16816(o[2 * d + 1], af, b2, b3, o[2 * d + 1]);
       }
     }
-    cs = cs + 1 == C::kStages ? 0 : cs + 1;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&B.empty[cs]);
+    if (++cs == C::kStages) {
+      cs = 0;
+      phase ^= 1;
+    }
 
     if (cur.t + 1 == cur.nt || x + 1 == x1) {
       // ---- the end of this CTA's part of the group: join the WK warps of each row tile pairwise
@@ -371,7 +418,7 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads, 1) attn_window_ke
           q[32 * (C::kOut + 2)] = la;
           q[32 * (C::kOut + 3)] = lb;
         }
-        __syncthreads();
+        named_bar(1, C::kWarps * 32);
         if (wk < h) {
           const float *q = join + (size_t)(wk * WM + wm) * 32 * (C::kOut + 4) + lane;
           const float m2a = q[32 * C::kOut], m2b = q[32 * (C::kOut + 1)];
@@ -388,7 +435,7 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads, 1) attn_window_ke
             o[i >> 2][i & 3] = (i & 2) ? o[i >> 2][i & 3] * f2 + v * f3 : o[i >> 2][i & 3] * f0 + v * f1;
           }
         }
-        __syncthreads();
+        named_bar(1, C::kWarps * 32);
       }
       const long long gs = x - cur.t, ge = gs + cur.nt;
       const bool whole = gs >= x0 && ge <= x1;
@@ -424,7 +471,7 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads, 1) attn_window_ke
         }
         // the shares that hold this group; each share is the first of at most one cut group, whose count it keeps
         const int c0 = (int)(((gs + 1) * shares - 1) / total), c1 = (int)((ge * shares - 1) / total);
-        __syncthreads();
+        named_bar(1, C::kWarps * 32);
         if (threadIdx.x == 0) {
           __threadfence();
           const uint32_t before = atomicAdd(a.counts + c0, 1u);
@@ -432,10 +479,10 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads, 1) attn_window_ke
           if (last_s) a.counts[c0] = 0;  // for the next call
           __threadfence();
         }
-        __syncthreads();
+        named_bar(1, C::kWarps * 32);
         if (last_s) {
           const bool late = gs > total * c0 / shares;  // the first part lies in slot 1
-          for (int i = threadIdx.x; i < live * (D / 2); i += C::kThreads) {
+          for (int i = threadIdx.x; i < live * (D / 2); i += C::kWarps * 32) {
             const int r = i / (D / 2), d = 2 * (i % (D / 2));
             float m = -INFINITY, l = 0.f, y0 = 0.f, y1 = 0.f;
 #pragma unroll 8
@@ -456,35 +503,49 @@ __global__ void __launch_bounds__(WinCfg<D, WM, WK>::kThreads, 1) attn_window_ke
             *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(y0 * inv, y1 * inv);
           }
         }
-        __syncthreads();
+        named_bar(1, C::kWarps * 32);
       }
     }
     cur.advance(a, groups);
   }
-  cp_async_wait_all();
 }
 
 template <int D, int WM, int WK>
-cudaError_t launch(WinArgs w, cudaStream_t s) {
+cudaError_t launch(WinArgs w, const moe_kv_cache &c, cudaStream_t s) {
   using C = WinCfg<D, WM, WK>;
+  CUtensorMap km, vm;
+  if (!make_pages_map(&km, c.k, c.n_pages, w.a, D) || !make_pages_map(&vm, c.v, c.n_pages, w.a, D))
+    return cudaErrorInvalidValue;
   w.row_tiles = (w.a.kv.per * w.a.G + C::kRows - 1) / C::kRows;
   cudaError_t err =
       cudaFuncSetAttribute(attn_window_kernel<D, WM, WK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (err != cudaSuccess) return err;
-  attn_window_kernel<D, WM, WK><<<kAttnShares, C::kThreads, C::kSmem, s>>>(w);
+  attn_window_kernel<D, WM, WK><<<kAttnShares, C::kThreads, C::kSmem, s>>>(km, vm, w);
   return cudaGetLastError();
 }
 
 // Rows of a window: one, two or four 16-row tiles side by side; more rows than 64 walk the keys again.
 template <int D>
-cudaError_t launch_d(const WinArgs &w, cudaStream_t s) {
+cudaError_t launch_d(const WinArgs &w, const moe_kv_cache &c, cudaStream_t s) {
   const int rows = w.a.kv.per * w.a.G;
-  if (rows <= 16) return launch<D, 1, 8>(w, s);
-  if (rows <= 32) return launch<D, 2, 4>(w, s);
-  return launch<D, 4, 2>(w, s);
+  if (rows <= 16) return launch<D, 1, 8>(w, c, s);
+  if (rows <= 32) return launch<D, 2, 4>(w, c, s);
+  return launch<D, 4, 2>(w, c, s);
 }
 
 }  // namespace
+
+bool make_pages_map(CUtensorMap *map, const uint16_t *cache, int n_pages, const AttnArgs &a, int D) {
+  auto fn = tma_encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)n_pages * a.V << a.kv.log_ps};  // rows below 2^31
+  const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
+  const cuuint32_t box[2] = {64, 1u << a.kv.log_ps};
+  const cuuint32_t one[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(cache), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 size_t attn_part_bytes(const moe_attn_dims &d, int, int) { return (size_t)kAttnShares * 2 * 64 * (d.head_dim + 2) * 4; }
 
@@ -493,8 +554,8 @@ cudaError_t launch_attn(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_
   trace_mark(MOE_KERNEL_ATTN, false, s);
   const bool window = !a.kv.q_start && a.kv.per <= 8;
   const cudaError_t err = !window             ? launch_attn_tc(d, a, c, s)
-                          : d.head_dim == 128 ? launch_d<128>(w, s)
-                                              : launch_d<64>(w, s);
+                          : d.head_dim == 128 ? launch_d<128>(w, c, s)
+                                              : launch_d<64>(w, c, s);
   trace_mark(MOE_KERNEL_ATTN, true, s);
   return err;
 }

@@ -1,6 +1,7 @@
 // Shared by the attention kernels: what they know of a batch, and small device helpers.
 #pragma once
 
+#include <cuda.h>
 #include <limits.h>
 
 #include "attn_index.h"
@@ -36,6 +37,8 @@ struct AttnArgs {
   uint32_t *counts;   // workspace header: parts that have come, zero between calls [kAttnShares]
 };
 
+// One side of the cache as rows of D elements, boxes of a page's rows x 64 elements, 128-byte swizzle.
+bool make_pages_map(CUtensorMap *map, const uint16_t *cache, int n_pages, const AttnArgs &a, int D);
 size_t attn_part_bytes(const moe_attn_dims &d, int n_seqs, int T);
 cudaError_t launch_attn_tc(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s);
 cudaError_t launch_attn(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s);

@@ -80,6 +80,9 @@ __device__ __forceinline__ uint64_t sdesc_n_sw128(uint32_t addr, uint32_t group_
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// The lowest n bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
 __device__ __forceinline__ float max_nan(float a, float b) {
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
@@ -182,13 +185,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     __syncwarp();
     const int ps = 1 << a.kv.log_ps, pages = kTcBK >> a.kv.log_ps;
-    bool live = true;
     int issued_k = 0, issued_v = 0;
     for (int t = 0; t < nt; ++t) {
       const int st = t % C::kStages, j0 = tile_of(tr, t) << kTcLogBK;
       const uint32_t ph = ((t / C::kStages) & 1) ^ 1;
-      if (live && !at_wait(&B.k_empty[st], ph, B, a.status)) live = false;
-      if (!live) break;
+      if (!__all_sync(0xffffffffu, at_wait(&B.k_empty[st], ph, B, a.status))) break;
       // lane l < pages: page l of the tile
       const int a0 = j0 + (lane << a.kv.log_ps), e0 = a0 + ps;
       const bool seen = lane < pages && a0 < s.n && a0 <= p1 &&
@@ -214,8 +215,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tma_load_2d(k_s + st * C::kTileBytes + h * C::kHalfBytes + lane * ps * 128, &kmap, h * 64, row, &B.k_full[st]);
       issued_k = t + 1;
       __syncwarp();
-      if (!at_wait(&B.v_empty[st], ph, B, a.status)) live = false;
-      if (!live) break;
+      if (!__all_sync(0xffffffffu, at_wait(&B.v_empty[st], ph, B, a.status))) break;
       if (lane == 0) mbar_arrive_expect_tx(&B.v_full[st], (uint32_t)(__popc(good) * ps * D * 2));
       __syncwarp();
       if (ok)
@@ -300,21 +300,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const bool live = j <= p1 && j < s.n && (a.window <= 0 || p0 - j < a.window || j < a.n_sinks) &&
                             !(in.bad[r >> 5] >> (r & 31) & 1);
           bool clear = !live;
-          if (live) {
-            for (int i = 0; i < C::kHalves * 8 && !clear; ++i) {
-              const uint4 x = *reinterpret_cast<const uint4 *>(v + (i >> 3) * C::kHalfBytes + r * 128 +
-                                                               (((i & 7) + r) & 7) * 16);
-              const uint32_t e[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                clear |= (e[k] & 0x7f80u) == 0x7f80u || (e[k] & 0x7f800000u) == 0x7f800000u;
-            }
+          for (int i = 0; i < C::kHalves * 8; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(v + (i >> 3) * C::kHalfBytes + r * 128 + (((i & 7) + r) & 7) * 16);
+            const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) clear |= (e[k] & 0x7f80u) == 0x7f80u || (e[k] & 0x7f800000u) == 0x7f800000u;
           }
           const uint32_t flag = __ballot_sync(0xffffffffu, live && clear);
           if (lane == 0) B.flagged[st][r0 >> 5] = flag;
           if (clear)
             for (int i = 0; i < C::kHalves * 8; ++i)
-              *reinterpret_cast<uint4 *>(v + (i >> 3) * C::kHalfBytes + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4 *>(v + (i >> 3) * C::kHalfBytes + r * 128 + (((i & 7) + r) & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
@@ -344,20 +341,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * c]));
         tmem_wait_ld();
-        bool poison = false;
+        uint32_t seen[4];
         if (in.partial) {
           // the keys of the tile that this row sees: columns up to hi, from lo on or below the sinks
-          const int hi = min(pos, s.n - 1) - j0;
-          const int lo = a.window > 0 ? pos - a.window + 1 - j0 : INT_MIN;
+          const int hi = min(pos, s.n - 1) - j0 + 1;
+          const int lo = a.window > 0 ? pos - a.window + 1 - j0 : 0;
           const int sk = a.window > 0 ? a.n_sinks - j0 : 0;
-          at_wait(&B.v_ready[st], (t / C::kStages) & 1, B, a.status);
           const float none = scale < 0.f ? INFINITY : -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 128; ++c) {
-            const bool v = c <= hi && (c >= lo || c < sk) && !(in.bad[c >> 5] >> (c & 31) & 1);
-            if (!v) x[c] = none;
-            poison |= v && (B.flagged[st][c >> 5] >> (c & 31) & 1);
-          }
+          for (int k = 0; k < 4; ++k)
+            seen[k] = (below(lo - 32 * k) ^ 0xffffffffu | below(sk - 32 * k)) & below(hi - 32 * k) & ~in.bad[k];
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (!(seen[c >> 5] >> (c & 31) & 1)) x[c] = none;
         }
         float mx;
         if (scale >= 0.f) {
@@ -417,7 +413,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tmem_st_32x32b_x16(ts + c / 2, p);
         }
         l += l0 + l1;
-        if (poison) l = NAN;
+        if (in.partial) {
+          // a value that is not finite was left out of P V: rows that see it become NaN
+          at_wait(&B.v_ready[st], (t / C::kStages) & 1, B, a.status);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (seen[k] & B.flagged[st][k]) l = NAN;
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -462,7 +464,6 @@ cudaError_t launch_tc(const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) 
   TcArgs w{a, kTcRows / a.G};
   auto fn = tma_encode_fn();
   if (!fn) return cudaErrorNotSupported;
-  const int ps = 1 << a.kv.log_ps;
   CUtensorMap qm, km, vm;
   const cuuint32_t one[3] = {1, 1, 1};
   {
@@ -474,15 +475,8 @@ cudaError_t launch_tc(const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) 
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  const int rows = c.n_pages * a.V * ps;  // below 2^31: checked on the host
-  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)ps};
-  for (int i = 0; i < 2; ++i)
-    if (fn(i ? &vm : &km, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(i ? a.v : a.k), dims, strides, box,
-           one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
+  if (!make_pages_map(&km, c.k, c.n_pages, a, D) || !make_pages_map(&vm, c.v, c.n_pages, a, D))
+    return cudaErrorInvalidValue;
   const int pair = 2 * w.tokens;
   const long long items = a.kv.q_start ? (long long)a.T / pair + std::min(a.T, a.kv.n_seqs)
                                        : (long long)a.kv.n_seqs * ((a.kv.per + pair - 1) / pair);

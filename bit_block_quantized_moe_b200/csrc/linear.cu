@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(LnCfg<BN>::kThreads, 1)
       const int c1 = (int)((long long)a.chunks * (ks + 1) / a.ks);
       for (int c = (int)((long long)a.chunks * ks / a.ks); c < c1; ++c, ++cnt) {
         const int s = cnt % C::kStages;
-        if (live && !ln_wait(&B.empty[s], ((cnt / C::kStages) & 1) ^ 1, B, a.status)) live = false;
+        if (live) live = __all_sync(0xffffffffu, ln_wait(&B.empty[s], ((cnt / C::kStages) & 1) ^ 1, B, a.status));
         if (!live) continue;
         issued = cnt + 1;
         if (elect_one()) {
