@@ -21,7 +21,8 @@ cudaError_t launch_qk_norm_rope(const moe_attn_dims &d, const uint16_t *qkv, int
                                 const float *gk, float eps, const moe_rope *rope, const moe_kv_cache &c,
                                 const KvArgs &kv, int T, uint16_t *q_out, uint32_t *status, cudaStream_t s);
 
-constexpr int kAttnShares = 148;  // CTAs among which a window call's key tiles are cut, one a SM
+constexpr int kAttnSms = 148;               // a window call has one or two CTAs a SM
+constexpr int kAttnShares = 4 * kAttnSms;   // the most shares into which its key tiles are cut
 
 struct AttnArgs {
   const uint16_t *q;
@@ -34,11 +35,12 @@ struct AttnArgs {
   uint16_t *out;
   uint32_t *status;
   float *part;        // workspace: parts of split groups
-  uint32_t *counts;   // workspace header: parts that have come, zero between calls [kAttnShares]
+  uint32_t *counts;   // workspace header: parts that have come [kAttnShares], then shares taken; zero between calls
 };
 
-// One side of the cache as rows of D elements, boxes of a page's rows x 64 elements, 128-byte swizzle.
-bool make_pages_map(CUtensorMap *map, const uint16_t *cache, int n_pages, const AttnArgs &a, int D);
+// One side of the cache as rows of D elements, boxes of a page's rows (at most `tile`) x 64 elements, 128-byte
+// swizzle.
+bool make_pages_map(CUtensorMap *map, const uint16_t *cache, int n_pages, const AttnArgs &a, int D, int tile);
 size_t attn_part_bytes(const moe_attn_dims &d, int n_seqs, int T);
 cudaError_t launch_attn_tc(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s);
 cudaError_t launch_attn(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s);

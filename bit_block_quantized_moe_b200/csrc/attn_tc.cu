@@ -475,7 +475,7 @@ cudaError_t launch_tc(const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) 
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  if (!make_pages_map(&km, c.k, c.n_pages, a, D) || !make_pages_map(&vm, c.v, c.n_pages, a, D))
+  if (!make_pages_map(&km, c.k, c.n_pages, a, D, kTcBK) || !make_pages_map(&vm, c.v, c.n_pages, a, D, kTcBK))
     return cudaErrorInvalidValue;
   const int pair = 2 * w.tokens;
   const long long items = a.kv.q_start ? (long long)a.T / pair + std::min(a.T, a.kv.n_seqs)
