@@ -6,16 +6,19 @@
 //   s_j = scale q.k_j,  m' = max(m, max_j s_j),  l' = l e^(m - m') + sum_j e^(s_j - m'),  o' = o e^(m - m') + ...
 // in base 2 with scale * log2(e) folded in.
 //
-// Split: all 64-key tiles of all (sequence, key/value head, row tile) groups stand in one line, which is cut into
+// Split: all key tiles of all (sequence, key/value head, row tile) groups stand in one line, which is cut into
 // equal shares whatever the lengths (they are read on the device, so that a captured graph follows them).  With work
 // for more than one share a CTA, the CTAs take the later shares as they come free.  A group that is cut leaves parts
 // (m, l, o) in the workspace; the CTA that brings the last one joins them in share order, so that the result does not
 // depend on which that is.
 //   last warp  : walks the line; TMA of K and V, a page at a time, into a ring of stages (128-byte swizzle); a group's
 //                queries, and a record of where the stage stands, beside it;
-//   8 warps    : the scores of 8 keys each, the weights to shared memory, then D/8 columns of the output each over all
-//                64 keys.  A warp's output is 8 registers a row tile, which leaves room for two CTAs a SM (one waits
-//                while the other computes), and a group's end needs no exchange but of the row sums.
+//   8 warps    : the scores of 1/8 of the keys each, the weights to shared memory, then D/8 columns of the output each
+//                over all keys.  A warp's output is few registers, which leaves room for two CTAs a SM (one waits
+//                while the other computes), and a group's end needs no exchange but of the row sums.  The running
+//                maximum is left as it is until some score exceeds it by 8 (a factor of 256, which fp32 sums and bf16
+//                weights carry without loss), so that a tile needs one meeting of the warps, which also tells them
+//                whether it is so.
 // Rows of V that no query of the window sees are masked in the registers that feed the product, so that nothing behind
 // them can reach an output.  Every wait is bounded (sync.cuh).
 #include <algorithm>
@@ -26,10 +29,9 @@
 namespace moe {
 namespace {
 
-constexpr int kBK = 64;         // keys a tile
-constexpr int kLogBK = 6;
-constexpr int kMinTiles = 1;    // tiles that a share has at least
-constexpr int kShareTiles = 16; // tiles that a share has at least where there are several a CTA
+constexpr int kMinTiles = 1;     // tiles that a share has at least
+constexpr int kShareTiles = 16;  // tiles that a share has at least where there are several a CTA
+constexpr float kWinLazy = 8.0f;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -54,31 +56,37 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
 
 template <int D, int MT>
 struct WinCfg {
+  static constexpr int kLogBK = D == 128 ? 6 : 7;   // keys a tile: 16 KB of K and of V
+  static constexpr int kBK = 1 << kLogBK;
   static constexpr int kWarps = 8;                  // beside the producer
+  static constexpr int kNK = kBK / 64;              // 8-key groups a warp
   static constexpr int kThreads = (kWarps + 1) * 32;
   static constexpr int kRows = 16 * MT;
   static constexpr int kCtas = MT == 1 ? 2 : 1;     // a SM
   static constexpr int kHalfBytes = kBK * 128;      // 64 columns of a tile, one swizzle row a key
   static constexpr int kTileBytes = kBK * D * 2;    // K or V of a stage
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = (MT == 1 ? 3 : MT == 2 ? 5 : 4) * (128 / D);
+  static constexpr int kStages = MT == 1 ? 3 : MT == 2 ? 5 : 4;
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kQAt = kStages * kStageBytes;
   static constexpr int kPAt = kQAt + kStages * kQBytes;
-  static constexpr int kSmem = kPAt + kRows * kBK * 2;
+  static constexpr int kPBytes = kRows * kBK * 2;
+  static constexpr int kSmem = kPAt + 2 * kPBytes;  // weights by turns: a warp may be one tile ahead
 };
+
+constexpr int kRecFirst = 1, kRecLast = 2;  // of this CTA's part of the group
+constexpr int kRecPartial = 4;               // some row does not see some key of the tile
+constexpr int kRecEnd = 8;                   // no tile: the CTA is done
 
 // What the producer tells beside a stage.
 struct TileRec {
   int b, hv, rt;      // the group: sequence, key/value head, row tile
   int j0, n;          // first key of the tile, keys of the sequence
-  int first, last;    // of this CTA's part of the group
   int q;              // with `first`: which of the places holds the group's queries
-  int partial;        // some row does not see some key of the tile
-  int end;            // no tile: the CTA is done
+  int flags;          // kRec...
   int share, c0, c1;  // this share, and the shares that hold the group
   int slot, slot0;    // where this share's part lies, and where that of c0 does
-  uint32_t bad[2];    // keys whose page is outside the cache
+  uint32_t bad[4];    // keys whose page is outside the cache
 };
 
 template <int STAGES>
@@ -94,15 +102,15 @@ struct WinArgs {
 };
 
 // The key tiles of a sequence; one in which nothing is seen where it is empty.
-__device__ __forceinline__ TileRange window_tiles(const AttnArgs &a, const SeqView &s) {
-  TileRange r = tile_range(s.n - s.m, s.n - 1, s.n, a.window, a.n_sinks, kLogBK);
+__device__ __forceinline__ TileRange window_tiles(const AttnArgs &a, const SeqView &s, int log_bk) {
+  TileRange r = tile_range(s.n - s.m, s.n - 1, s.n, a.window, a.n_sinks, log_bk);
   if (r.count < 1) r.count = 1;
   return r;
 }
 
-__device__ __forceinline__ int window_count(const AttnArgs &a, int b) {
+__device__ __forceinline__ int window_count(const AttnArgs &a, int b, int log_bk) {
   if (b >= a.kv.n_seqs) return 0;
-  return window_tiles(a, seq_view(nullptr, a.kv.kv_len, b, a.kv.per, a.T, a.kv.cap)).count;
+  return window_tiles(a, seq_view(nullptr, a.kv.kv_len, b, a.kv.per, a.T, a.kv.cap), log_bk).count;
 }
 
 template <class Bars>
@@ -167,8 +175,8 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
   extern __shared__ __align__(1024) uint8_t win_smem[];
   __shared__ WinBars<C::kStages> B;
   __shared__ long long sum_s[C::kThreads / 32];
-  __shared__ __align__(16) float max_s[C::kRows][C::kWarps], sum_r[C::kRows][C::kWarps];
-  __shared__ __align__(8) uint8_t use_s[2][C::kWarps];  // by turns: a warp may be one tile ahead
+  __shared__ __align__(16) float row_s[C::kRows][C::kWarps];  // maxima, or sums, of each row by warp
+  __shared__ __align__(16) uint8_t use_s[2][16];  // by turns: a warp may be one tile ahead
   __shared__ int last_s;
   const AttnArgs &a = w.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -186,7 +194,7 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
   // ---- the length of the line, and its shares
   if (blockIdx.x == 0) check_sequences(a.kv, a.T, a.status);
   long long total = 0;
-  for (int b = threadIdx.x; b < a.kv.n_seqs; b += C::kThreads) total += window_count(a, b);
+  for (int b = threadIdx.x; b < a.kv.n_seqs; b += C::kThreads) total += window_count(a, b, C::kLogBK);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   if (lane == 0) sum_s[warp] = total;
@@ -201,7 +209,7 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
   if (warp == C::kWarps) {
     // ---- producer: all but the pieces is uniform over the warp ----
     // lane l < pieces has piece l of a tile: a page, or half of one of 128
-    const int log_pc = min(a.kv.log_ps, kLogBK), pc = 1 << log_pc, pieces = kBK >> log_pc;
+    const int log_pc = min(a.kv.log_ps, C::kLogBK), pc = 1 << log_pc, pieces = C::kBK >> log_pc;
     int st = 0, qn = 0, b = 0, share = blockIdx.x;
     uint32_t ph = 1;
     long long issued = 0, line = 0;  // line: tiles before sequence b
@@ -213,7 +221,7 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
       const long long x0 = mul_div(total, share, shares), x1 = mul_div(total, share + 1, shares);
       // the sequence of x0: at or after the last share's
       for (;;) {
-        long long incl = window_count(a, b + lane);
+        long long incl = window_count(a, b + lane, C::kLogBK);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const long long y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -228,32 +236,39 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
       }
       if (b >= a.kv.n_seqs) break;  // only where the lengths change under the call
       SeqView s = seq_view(nullptr, a.kv.kv_len, b, a.kv.per, a.T, a.kv.cap);
-      TileRange r = window_tiles(a, s);
-      int gi = (int)mul_div(x0 - line, 1, r.count);
+      TileRange r = window_tiles(a, s, C::kLogBK);
+      const int gi = (int)mul_div(x0 - line, 1, r.count);
       int t = (int)(x0 - line - (long long)gi * r.count);
       int hv = gi / w.row_tiles, rt = gi - hv * w.row_tiles;
+      // this lane's piece of the tile at the cursor
+      auto piece = [&](bool &seen) {
+        const int a0 = (tile_of(r, t) << C::kLogBK) + (lane << log_pc), e0 = a0 + pc;
+        seen = lane < pieces && a0 < s.n && (a.window <= 0 || e0 - 1 > s.n - s.m - a.window || a0 < a.n_sinks);
+        return seen ? __ldg(a.kv.table + (size_t)b * a.kv.max_pages + (a0 >> a.kv.log_ps)) : 0;
+      };
+      bool seen;
+      int page = piece(seen);
       for (long long x = x0; x < x1; ++x) {
-        const int j0 = tile_of(r, t) << kLogBK, n = s.n, p0 = n - s.m;
-        const int a0 = j0 + (lane << log_pc), e0 = a0 + pc;
-        const bool seen = lane < pieces && a0 < n && (a.window <= 0 || e0 - 1 > p0 - a.window || a0 < a.n_sinks);
-        const int page = seen ? __ldg(a.kv.table + (size_t)b * a.kv.max_pages + (a0 >> a.kv.log_ps)) : 0;
-        const bool ok = seen && page >= 0 && page < a.kv.n_pages;
-        const uint32_t good = __ballot_sync(0xffffffffu, ok), wrong = __ballot_sync(0xffffffffu, seen && !ok);
         live = __all_sync(0xffffffffu, win_wait(&B.empty[st], ph, B, a.status));
         if (!live) break;
+        const bool ok = seen && page >= 0 && page < a.kv.n_pages;
+        const uint32_t good = __ballot_sync(0xffffffffu, ok), wrong = __ballot_sync(0xffffffffu, seen && !ok);
+        const bool first = x == x0 || t == 0;
+        const int j0 = tile_of(r, t) << C::kLogBK, cb = b, chv = hv, crt = rt;
+        // below 2^31: checked on the host
+        const int row = ((page * a.V + hv) << a.kv.log_ps) + ((j0 + (lane << log_pc)) & ((1 << a.kv.log_ps) - 1));
         if (lane == 0) {
           TileRec &rec = B.rec[st];
+          const bool last = x + 1 == x1 || t + 1 == r.count;
           rec.b = b;
           rec.hv = hv;
           rec.rt = rt;
           rec.j0 = j0;
-          rec.n = n;
-          rec.first = x == x0 || t == 0;
+          rec.n = s.n;
           rec.q = qn;
-          rec.last = x + 1 == x1 || t + 1 == r.count;
-          rec.partial = wrong || !tile_full(p0, n - 1, j0, kBK, n, a.window, a.n_sinks);
-          rec.end = 0;
-          if (rec.last) {
+          rec.flags = (first ? kRecFirst : 0) | (last ? kRecLast : 0) |
+                      (wrong || !tile_full(s.n - s.m, s.n - 1, j0, C::kBK, s.n, a.window, a.n_sinks) ? kRecPartial : 0);
+          if (last) {
             const long long gs = x - t, ge = gs + r.count;
             rec.share = share;
             rec.c0 = gs >= x0 ? share : share_of(gs, shares, total);
@@ -261,32 +276,16 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
             rec.slot = gs > x0;
             rec.slot0 = gs > (gs >= x0 ? x0 : mul_div(total, rec.c0, shares));
           }
-          rec.bad[0] = rec.bad[1] = 0;
+          rec.bad[0] = rec.bad[1] = rec.bad[2] = rec.bad[3] = 0;
           if (wrong) {
-            for (int k = 0; k < kBK; ++k)
+            for (int k = 0; k < C::kBK; ++k)
               if (wrong >> (k >> log_pc) & 1) rec.bad[k >> 5] |= 1u << (k & 31);
             set_status(a.status, kStatusBadIndex);
           }
           mbar_arrive_expect_tx(&B.full[st], (uint32_t)(__popc(good) * pc * D * 4));
         }
         __syncwarp();
-        if (x == x0 || t == 0) {
-          // the group's queries; rows behind the last are zeros.  The groups in flight are no more than the stages,
-          // so that as many places in turn suffice.
-          constexpr int kChunks = D / 8;
-          const uint32_t dst = smem0 + C::kQAt + (uint32_t)qn * C::kQBytes;
-          qn = qn + 1 == C::kStages ? 0 : qn + 1;
-          for (int i = lane; i < C::kRows * kChunks; i += 32) {
-            const int r = i / kChunks, ch = i % kChunks, rg = rt * C::kRows + r, tok = rg / a.G;
-            const bool in = rg < rows;
-            const uint16_t *src = a.q + (in ? (size_t)(b * a.kv.per + tok) * a.ld_q + (size_t)(hv * a.G + rg - tok * a.G) * D + ch * 8 : 0);
-            cp_async16_or_zero(dst + (uint32_t)(r * kChunks + (ch ^ (r & 7))) * 16u, src, in);
-          }
-        }
-        cp_async_arrive(&B.full[st]);  // every lane, when its copies have landed
         if (ok) {
-          // below 2^31: checked on the host
-          const int row = ((page * a.V + hv) << a.kv.log_ps) + (a0 & ((1 << a.kv.log_ps) - 1));
           uint8_t *dst = win_smem + st * C::kStageBytes + lane * pc * 128;
 #pragma unroll
           for (int h = 0; h < D / 64; ++h) {
@@ -295,11 +294,7 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
           }
         }
         __syncwarp();
-        ++issued;
-        if (++st == C::kStages) {
-          st = 0;
-          ph ^= 1;
-        }
+        // the cursor, and the next tile's pages, which come in while this warp waits for a stage
         if (++t == r.count) {
           t = 0;
           if (++rt == w.row_tiles) {
@@ -309,10 +304,29 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
               if (x + 1 < x1) {
                 line += (long long)r.count * groups;
                 s = seq_view(nullptr, a.kv.kv_len, ++b, a.kv.per, a.T, a.kv.cap);
-                r = window_tiles(a, s);
+                r = window_tiles(a, s, C::kLogBK);
               }
             }
           }
+        }
+        if (x + 1 < x1) page = piece(seen);
+        if (first) {
+          // the group's queries; rows behind the last are zeros.  The groups in flight are no more than the stages,
+          // so that as many places in turn suffice.
+          const uint32_t dst = smem0 + C::kQAt + (uint32_t)qn * C::kQBytes;
+          qn = qn + 1 == C::kStages ? 0 : qn + 1;
+          for (int i = lane; i < C::kRows * kChunks; i += 32) {
+            const int rr = i / kChunks, ch = i % kChunks, rg = crt * C::kRows + rr, tok = rg / a.G;
+            const bool in = rg < rows;
+            const uint16_t *src = a.q + (in ? (size_t)(cb * a.kv.per + tok) * a.ld_q + (size_t)(chv * a.G + rg - tok * a.G) * D + ch * 8 : 0);
+            cp_async16_or_zero(dst + (uint32_t)(rr * kChunks + (ch ^ (rr & 7))) * 16u, src, in);
+          }
+        }
+        cp_async_arrive(&B.full[st]);  // every lane, when its copies have landed
+        ++issued;
+        if (++st == C::kStages) {
+          st = 0;
+          ph ^= 1;
         }
       }
       if (shares <= (int)gridDim.x) break;
@@ -325,7 +339,7 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
     const bool told = __all_sync(0xffffffffu, win_wait(&B.empty[st], ph, B, a.status));
     if (told) {
       if (lane == 0) {
-        B.rec[st].end = 1;
+        B.rec[st].flags = kRecEnd;
         mbar_arrive(&B.full[st]);
       }
       __syncwarp();
@@ -333,8 +347,8 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
     }
     // every copy issued must land before the CTA exits, also after an abort
     const int open = C::kStages - (told ? 1 : 0);
-    for (long long t = issued > open ? issued - open : 0; t < issued; ++t)
-      if (!mbar_wait(&B.full[t % C::kStages], (uint32_t)(t / C::kStages) & 1)) set_status(a.status, kStatusTimeout);
+    for (long long i = issued > open ? issued - open : 0; i < issued; ++i)
+      if (!mbar_wait(&B.full[i % C::kStages], (uint32_t)(i / C::kStages) & 1)) set_status(a.status, kStatusTimeout);
     return;
   }
 
@@ -348,13 +362,12 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
   for (;;) {
     const bool came = win_wait(&B.full[cs], phase, B, a.status);
     const TileRec &rec = B.rec[cs];
-    const bool end = came && rec.end;
-    const uint32_t st = smem0 + (uint32_t)cs * C::kStageBytes;
-    const int n = rec.n, j0 = rec.j0, base_pos = n - a.kv.per, r0 = rec.rt * C::kRows;
-    const bool partial = rec.partial;
-    float sc[MT][4];
-    if (came && !end) {
-      if (rec.first) {
+    const int flags = came ? rec.flags : kRecEnd;
+    const uint32_t st = smem0 + (uint32_t)cs * C::kStageBytes, ps = smem0 + C::kPAt + (uint32_t)turn * C::kPBytes;
+    float sc[MT][C::kNK][4];
+    bool grow = flags & kRecEnd;
+    if (!grow) {
+      if (flags & kRecFirst) {
         qs = smem0 + C::kQAt + (uint32_t)rec.q * C::kQBytes;
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
@@ -371,165 +384,211 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
                     qf[k][3]);
         }
       }
-      // ---- scores of this warp's 8 keys
-      uint32_t kf[D / 16][2];
-      const int r = 8 * warp + (lane & 7);
+      // ---- scores of this warp's keys
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        const int ch = 4 * k + (lane >> 3);
-        ldsm_x4(st + (uint32_t)((ch >> 3) * C::kHalfBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4)), kf[2 * k][0],
-                kf[2 * k][1], kf[2 * k + 1][0], kf[2 * k + 1][1]);
-      }
+      for (int nk = 0; nk < C::kNK; ++nk) {
+        uint32_t kf[D / 16][2];
+        const int r = 8 * (C::kNK * warp + nk) + (lane & 7);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t af[4];
-          if constexpr (MT == 1) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) af[e] = qf[k][e];
-          } else {
-            const int rq = 16 * i + (lane & 15);
-            ldsm_x4(qs + (uint32_t)(rq * kChunks + ((2 * k + (lane >> 4)) ^ (rq & 7))) * 16u, af[0], af[1], af[2], af[3]);
-          }
-          if (k & 1)
-            mma_bf16_16816(s1, af, kf[k][0], kf[k][1], s1);
-          else
-            mma_bf16_16816(s0, af, kf[k][0], kf[k][1], s0);
+        for (int k = 0; k < D / 32; ++k) {
+          const int ch = 4 * k + (lane >> 3);
+          ldsm_x4(st + (uint32_t)((ch >> 3) * C::kHalfBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4)), kf[2 * k][0],
+                  kf[2 * k][1], kf[2 * k + 1][0], kf[2 * k + 1][1]);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[i][e] = (s0[e] + s1[e]) * a.scale_log2;
+        for (int i = 0; i < MT; ++i) {
+          float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t af[4];
+            if constexpr (MT == 1) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) af[e] = qf[k][e];
+            } else {
+              const int rq = 16 * i + (lane & 15);
+              ldsm_x4(qs + (uint32_t)(rq * kChunks + ((2 * k + (lane >> 4)) ^ (rq & 7))) * 16u, af[0], af[1], af[2], af[3]);
+            }
+            if (k & 1)
+              mma_bf16_16816(s1, af, kf[k][0], kf[k][1], s1);
+            else
+              mma_bf16_16816(s0, af, kf[k][0], kf[k][1], s0);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[i][nk][e] = (s0[e] + s1[e]) * a.scale_log2;
+        }
       }
-      if (partial) {
+      if (flags & kRecPartial) {
         // which of the warp's keys some row sees, and of these the ones whose values are not finite: 0 * v is NaN
         // then, so that where rows differ in what they see such a key is left out of the product, and the rows that
         // see it become NaN
-        const int kk = 8 * warp + (lane >> 2), j = j0 + kk;
-        const bool live = j < n && (a.window <= 0 || base_pos - j < a.window || j < a.n_sinks) &&
-                          !(rec.bad[kk >> 5] >> (kk & 31) & 1);
-        bool bad = false;
-        if (live && a.kv.per > 1) {
-          const uint8_t *v = win_smem + cs * C::kStageBytes + C::kTileBytes + kk * 128;
+        const int n = rec.n, j0 = rec.j0, base_pos = n - a.kv.per, r0 = rec.rt * C::kRows;
 #pragma unroll
-          for (int i = 0; i < kChunks / 4; ++i) {
-            const int ch = 4 * i + (lane & 3);
-            bad |= not_finite8(*reinterpret_cast<const uint4 *>(v + (ch >> 3) * C::kHalfBytes + (((ch & 7) ^ (kk & 7)) << 4)));
-          }
-        }
-        const uint32_t lv = __ballot_sync(0xffffffffu, live);
-        uint32_t bd = __ballot_sync(0xffffffffu, bad);  // a key's bits: lanes 4k .. 4k + 3
-        bd |= bd >> 1;
-        bd |= bd >> 2;
-        uint32_t use = 0;
+        for (int nk = 0; nk < C::kNK; ++nk) {
+          const int k0 = 8 * (C::kNK * warp + nk), kk = k0 + (lane >> 2), j = j0 + kk;
+          const bool live = j < n && (a.window <= 0 || base_pos - j < a.window || j < a.n_sinks) &&
+                            !(rec.bad[kk >> 5] >> (kk & 31) & 1);
+          bool bad = false;
+          if (live && a.kv.per > 1) {
+            const uint8_t *v = win_smem + cs * C::kStageBytes + C::kTileBytes + kk * 128;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) use |= ((lv & ~bd) >> (4 * k) & 1) << k;
-        if (lane == 0) use_s[turn][warp] = (uint8_t)use;
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int rg = r0 + 16 * i + g + 8 * h;
-            const int pos = rg < rows ? base_pos + rg / a.G : -1;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int key = 2 * c + e;
-              const bool v = (lv >> (4 * key) & 1) && key_seen(pos, j0 + 8 * warp + key, n, a.window, a.n_sinks);
-              if (v && (bd >> (4 * key) & 1)) l[i][h] = NAN;
-              if (!v) sc[i][2 * h + e] = -INFINITY;
+            for (int i = 0; i < kChunks / 4; ++i) {
+              const int ch = 4 * i + (lane & 3);
+              bad |= not_finite8(*reinterpret_cast<const uint4 *>(v + (ch >> 3) * C::kHalfBytes + (((ch & 7) ^ (kk & 7)) << 4)));
             }
           }
+          const uint32_t lv = __ballot_sync(0xffffffffu, live);
+          uint32_t bd = __ballot_sync(0xffffffffu, bad);  // a key's bits: lanes 4k .. 4k + 3
+          bd |= bd >> 1;
+          bd |= bd >> 2;
+          uint32_t use = 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) use |= ((lv & ~bd) >> (4 * k) & 1) << k;
+          if (lane == 0) use_s[turn][C::kNK * warp + nk] = (uint8_t)use;
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int rg = r0 + 16 * i + g + 8 * h;
+              const int pos = rg < rows ? base_pos + rg / a.G : -1;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int key = 2 * c + e;
+                const bool v = (lv >> (4 * key) & 1) && key_seen(pos, j0 + k0 + key, n, a.window, a.n_sinks);
+                if (v && (bd >> (4 * key) & 1)) l[i][h] = NAN;
+                if (!v) sc[i][nk][2 * h + e] = -INFINITY;
+              }
+            }
+        }
       }
+    }
+    // ---- weights, with the maximum as it stands
+    auto weights = [&](int i, int h) {
+      const int r = 16 * i + g + 8 * h;
+      const float sub = m[i][h] == -INFINITY ? 0.f : m[i][h];  // nothing seen yet: 2^(-inf - 0) = 0
+      float sum = 0.f;
+#pragma unroll
+      for (int nk = 0; nk < C::kNK; ++nk) {
+        const float e0 = ex2(sc[i][nk][2 * h] - sub), e1 = ex2(sc[i][nk][2 * h + 1] - sub);
+        sum += e0 + e1;
+        const int ch = C::kNK * warp + nk;
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(ps + (uint32_t)(r * (2 * C::kBK) + ((ch ^ (r & 7)) << 4) + 4 * c)),
+                     "r"(pack_bf16x2(e0, e1))
+                     : "memory");
+      }
+      return sum;
+    };
+    float sums[MT][2];
+    if (!(flags & kRecEnd)) {
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float x = fmaxf(sc[i][2 * h], sc[i][2 * h + 1]);
+          const float most = m[i][h] + kWinLazy;
+#pragma unroll
+          for (int nk = 0; nk < C::kNK; ++nk) grow |= !(sc[i][nk][2 * h] <= most) || !(sc[i][nk][2 * h + 1] <= most);
+          sums[i][h] = weights(i, h);
+        }
+    }
+    // the meeting: the weights are there, unless a maximum has to grow (or the end has come)
+    if (win_meet(grow, kMeet)) {
+      if (win_meet(!came, kMeet) || (flags & kRecEnd)) break;  // all leave together when a wait has given up
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x = fmaxf(sc[i][0][2 * h], sc[i][0][2 * h + 1]);
+          if constexpr (C::kNK == 2) x = fmaxf(x, fmaxf(sc[i][C::kNK - 1][2 * h], sc[i][C::kNK - 1][2 * h + 1]));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          if (c == 0) max_s[16 * i + g + 8 * h][warp] = x;
+          if (c == 0) row_s[16 * i + g + 8 * h][warp] = x;
+        }
+      win_meet(false, kMeet);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 16 * i + g + 8 * h;
+          const float4 x0 = *reinterpret_cast<const float4 *>(&row_s[r][0]), x1 = *reinterpret_cast<const float4 *>(&row_s[r][4]);
+          const float mx = fmaxf(fmaxf(fmaxf(x0.x, x0.y), fmaxf(x0.z, x0.w)), fmaxf(fmaxf(x1.x, x1.y), fmaxf(x1.z, x1.w)));
+          const float nm = fmaxf(m[i][h], mx);
+          const float f = ex2(m[i][h] - (nm == -INFINITY ? 0.f : nm));
+          m[i][h] = nm;
+          l[i][h] *= f;
+#pragma unroll
+          for (int t = 0; t < kNT; ++t) {
+            o[i][t][2 * h] *= f;
+            o[i][t][2 * h + 1] *= f;
+          }
+          sums[i][h] = weights(i, h);
+        }
+      win_meet(false, kMeet);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      l[i][0] += sums[i][0];
+      l[i][1] += sums[i][1];
+    }
+    // ---- products: V fragments of this warp's columns, two 16-key steps a round
+#pragma unroll
+    for (int k = 0; k < C::kBK / 16; k += 2) {
+      uint32_t vf[2][kNT][2];
+      if constexpr (kNT == 2) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 16 * (k + e) + (lane & 15), ch = 2 * warp + (lane >> 4);
+          ldsm_x4_t(st + (uint32_t)(C::kTileBytes + (ch >> 3) * C::kHalfBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
+                    vf[e][0][0], vf[e][0][1], vf[e][kNT - 1][0], vf[e][kNT - 1][1]);
+        }
+      } else {
+        const int r = 16 * k + lane;
+        ldsm_x4_t(st + (uint32_t)(C::kTileBytes + r * 128 + ((warp ^ (r & 7)) << 4)), vf[0][0][0], vf[0][0][1],
+                  vf[1][0][0], vf[1][0][1]);
+      }
+      if (flags & kRecPartial) {
+        const uint32_t use = *reinterpret_cast<const volatile uint32_t *>(&use_s[turn][2 * k]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // this lane's keys of the two halves of a fragment: 2c, 2c + 1 and 8 more
+          const uint32_t u = use >> (16 * e + 2 * c);
+          const uint32_t v0 = (u & 1 ? 0xffffu : 0u) | (u & 2 ? 0xffff0000u : 0u);
+          const uint32_t v1 = (u & 256 ? 0xffffu : 0u) | (u & 512 ? 0xffff0000u : 0u);
+#pragma unroll
+          for (int t = 0; t < kNT; ++t) {
+            vf[e][t][0] &= v0;
+            vf[e][t][1] &= v1;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 16 * i + (lane & 15);
+          uint32_t af[4];
+          ldsm_x4(ps + (uint32_t)(r * (2 * C::kBK) + (((2 * (k + e) + (lane >> 4)) ^ (r & 7)) << 4)), af[0], af[1], af[2], af[3]);
+#pragma unroll
+          for (int t = 0; t < kNT; ++t) mma_bf16_16816(o[i][t], af, vf[e][t][0], vf[e][t][1], o[i][t]);
         }
     }
-    // the first meeting: maxima are there; all leave together when a wait has given up
-    if (win_meet(!came, kMeet) || end) break;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 16 * i + g + 8 * h;
-        const float4 x0 = *reinterpret_cast<const float4 *>(&max_s[r][0]), x1 = *reinterpret_cast<const float4 *>(&max_s[r][4]);
-        const float mx = fmaxf(fmaxf(fmaxf(x0.x, x0.y), fmaxf(x0.z, x0.w)), fmaxf(fmaxf(x1.x, x1.y), fmaxf(x1.z, x1.w)));
-        const float nm = fmaxf(m[i][h], mx);
-        const float sub = nm == -INFINITY ? 0.f : nm;  // nothing seen yet: 2^(-inf - 0) = 0
-        const float f = ex2(m[i][h] - sub);
-        m[i][h] = nm;
-        const float e0 = ex2(sc[i][2 * h] - sub), e1 = ex2(sc[i][2 * h + 1] - sub);
-        l[i][h] = l[i][h] * f + (e0 + e1);
-#pragma unroll
-        for (int t = 0; t < kNT; ++t) {
-          o[i][t][2 * h] *= f;
-          o[i][t][2 * h + 1] *= f;
-        }
-        *reinterpret_cast<uint32_t *>(win_smem + C::kPAt + r * 128 + ((warp ^ (r & 7)) << 4) + 4 * c) = pack_bf16x2(e0, e1);
-      }
-    win_meet(false, kMeet);  // the second: weights are there
-    {
-      unsigned long long use = ~0ull;
-      if (partial) use = *reinterpret_cast<const volatile unsigned long long *>(use_s[turn]);
-      turn ^= 1;
-      // V fragments of this warp's columns, two 16-key steps a round
-#pragma unroll
-      for (int k = 0; k < kBK / 16; k += 2) {
-        uint32_t vf[2][kNT][2];
-        if constexpr (kNT == 2) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = 16 * (k + e) + (lane & 15), ch = 2 * warp + (lane >> 4);
-            ldsm_x4_t(st + (uint32_t)(C::kTileBytes + (ch >> 3) * C::kHalfBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
-                      vf[e][0][0], vf[e][0][1], vf[e][1][0], vf[e][1][1]);
-          }
-        } else {
-          const int r = 16 * k + lane;
-          ldsm_x4_t(st + (uint32_t)(C::kTileBytes + r * 128 + ((warp ^ (r & 7)) << 4)), vf[0][0][0], vf[0][0][1],
-                    vf[1][0][0], vf[1][0][1]);
-        }
-        if (partial) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // this lane's keys of the two halves of a fragment: 2c, 2c + 1 and 8 more
-            const uint32_t u = (uint32_t)(use >> (16 * (k + e) + 2 * c));
-            const uint32_t v0 = (u & 1 ? 0xffffu : 0u) | (u & 2 ? 0xffff0000u : 0u);
-            const uint32_t v1 = (u & 256 ? 0xffffu : 0u) | (u & 512 ? 0xffff0000u : 0u);
-#pragma unroll
-            for (int t = 0; t < kNT; ++t) {
-              vf[e][t][0] &= v0;
-              vf[e][t][1] &= v1;
-            }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = 16 * i + (lane & 15);
-            uint32_t af[4];
-            ldsm_x4(smem0 + C::kPAt + (uint32_t)(r * 128 + (((2 * (k + e) + (lane >> 4)) ^ (r & 7)) << 4)), af[0], af[1],
-                    af[2], af[3]);
-#pragma unroll
-            for (int t = 0; t < kNT; ++t) mma_bf16_16816(o[i][t], af, vf[e][t][0], vf[e][t][1], o[i][t]);
-          }
-      }
+    turn ^= 1;
+    int share = 0, c0 = 0, c1 = 0, slot = 0, slot0 = 0, hv = 0, q0 = 0, r0 = 0;
+    if (flags & kRecLast) {
+      share = rec.share;
+      c0 = rec.c0;
+      c1 = rec.c1;
+      slot = rec.slot;
+      slot0 = rec.slot0;
+      hv = rec.hv;
+      q0 = rec.b * a.kv.per;
+      r0 = rec.rt * C::kRows;
     }
-    const bool last = rec.last;
-    const int share = rec.share, c0 = rec.c0, c1 = rec.c1, slot = rec.slot, slot0 = rec.slot0, hv = rec.hv;
-    const int q0 = rec.b * a.kv.per;
     __syncwarp();
     if (lane == 0) mbar_arrive(&B.empty[cs]);
     if (++cs == C::kStages) {
       cs = 0;
       phase ^= 1;
     }
-    if (!last) continue;
+    if (!(flags & kRecLast)) continue;
 
     // ---- the end of this CTA's part of the group: row sums over the warps, in warp order
 #pragma unroll
@@ -539,7 +598,7 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
         float x = l[i][h];
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
-        if (c == 0) sum_r[16 * i + g + 8 * h][warp] = x;
+        if (c == 0) row_s[16 * i + g + 8 * h][warp] = x;
       }
     win_meet(false, kMeet);
     const int live = min(rows - r0, C::kRows);
@@ -551,7 +610,7 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
       for (int h = 0; h < 2; ++h) {
         const int r = 16 * i + g + 8 * h, rg = r0 + r, col = warp * (8 * kNT) + 2 * c;
         if (r >= live) continue;
-        const float4 x0 = *reinterpret_cast<const float4 *>(&sum_r[r][0]), x1 = *reinterpret_cast<const float4 *>(&sum_r[r][4]);
+        const float4 x0 = *reinterpret_cast<const float4 *>(&row_s[r][0]), x1 = *reinterpret_cast<const float4 *>(&row_s[r][4]);
         const float sum = ((x0.x + x0.y) + (x0.z + x0.w)) + ((x1.x + x1.y) + (x1.z + x1.w));
         if (c0 == c1) {
           const float inv = sum == 0.f ? 0.f : 1.0f / sum;
@@ -621,7 +680,8 @@ template <int D, int MT>
 cudaError_t launch(WinArgs w, const moe_kv_cache &c, cudaStream_t s) {
   using C = WinCfg<D, MT>;
   CUtensorMap km, vm;
-  if (!make_pages_map(&km, c.k, c.n_pages, w.a, D, kBK) || !make_pages_map(&vm, c.v, c.n_pages, w.a, D, kBK))
+  if (!make_pages_map(&km, c.k, c.n_pages, w.a, D, C::kBK) ||
+      !make_pages_map(&vm, c.v, c.n_pages, w.a, D, C::kBK))
     return cudaErrorInvalidValue;
   w.row_tiles = (w.a.kv.per * w.a.G + C::kRows - 1) / C::kRows;
   cudaError_t err = cudaFuncSetAttribute(attn_window_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
