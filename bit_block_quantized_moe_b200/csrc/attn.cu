@@ -1,26 +1,26 @@
 // Attention of verify windows (1 to 8 new tokens a sequence) over the paged cache, on the legacy tensor path
-// (mma.sync): the work is reading the cache once, and a window's few rows fill 16-row products, not 128-row ones.
+// (mma.sync): the work is reading the cache once, and a window's few rows fill products 8 rows wide, not 128.
 //
 // The query heads of a group share their key/value head, so that a tile's rows are (token, head of the group) pairs:
 // row r is token r / G, head r % G.  One pass over the keys with the running maximum and sum of the softmax:
 //   s_j = scale q.k_j,  m' = max(m, max_j s_j),  l' = l e^(m - m') + sum_j e^(s_j - m'),  o' = o e^(m - m') + ...
-// in base 2 with scale * log2(e) folded in.
+// in base 2 with scale * log2(e) folded in.  Both products have the keys or the head dimension on the 16-row side and
+// the query rows on the 8-column side (S^T = K Q^T, O^T = V^T P^T).
 //
-// Split: all key tiles of all (sequence, key/value head, row tile) groups stand in one line, which is cut into
-// equal shares whatever the lengths (they are read on the device, so that a captured graph follows them).  With work
-// for more than one share a CTA, the CTAs take the later shares as they come free.  A group that is cut leaves parts
-// (m, l, o) in the workspace; the CTA that brings the last one joins them in share order, so that the result does not
-// depend on which that is.
+// Split: all key tiles of all (sequence, key/value head, row tile) groups stand in one line, which is cut into equal
+// shares, one a CTA, whatever the lengths (they are read on the device, so that a captured graph follows them).
+// (Smaller shares taken as CTAs come free were slower: every share's ends cost more than the balance gave.)  A group
+// that is cut leaves parts (m, l, o) in the workspace; the CTA that brings the last one joins them in share order, so
+// that the result does not depend on which that is.
 //   last warp  : walks the line; TMA of K and V, a page at a time, into a ring of stages (128-byte swizzle); a group's
 //                queries, and a record of where the stage stands, beside it;
-//   8 warps    : the scores of 1/8 of the keys each, the weights to shared memory, then D/8 columns of the output each
-//                over all keys.  A warp's output is few registers, which leaves room for two CTAs a SM (one waits
-//                while the other computes), and a group's end needs no exchange but of the row sums.  The running
+//   4 warps    : the scores of a quarter of the keys each, the weights to shared memory, then a quarter of the output's
+//                columns each over all keys, so that a group's end needs no exchange but of the row sums.  The running
 //                maximum is left as it is until some score exceeds it by 8 (a factor of 256, which fp32 sums and bf16
 //                weights carry without loss), so that a tile needs one meeting of the warps, which also tells them
-//                whether it is so.
-// Rows of V that no query of the window sees are masked in the registers that feed the product, so that nothing behind
-// them can reach an output.  Every wait is bounded (sync.cuh).
+//                whether it is so.  Two CTAs a SM: one computes while the other waits.
+// Values of keys that no query of the window sees are masked in the registers that feed the product, so that nothing
+// behind them can reach an output.  Every wait is bounded (sync.cuh).
 #include <algorithm>
 
 #include "attn.cuh"
@@ -29,8 +29,6 @@
 namespace moe {
 namespace {
 
-constexpr int kMinTiles = 1;     // tiles that a share has at least
-constexpr int kShareTiles = 16;  // tiles that a share has at least where there are several a CTA
 constexpr float kWinLazy = 8.0f;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
@@ -54,24 +52,26 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-template <int D, int MT>
+template <int D, int NR>
 struct WinCfg {
   static constexpr int kLogBK = D == 128 ? 6 : 7;   // keys a tile: 16 KB of K and of V
   static constexpr int kBK = 1 << kLogBK;
-  static constexpr int kWarps = 8;                  // beside the producer
-  static constexpr int kNK = kBK / 64;              // 8-key groups a warp
+  static constexpr int kWarps = 4;                  // beside the producer
   static constexpr int kThreads = (kWarps + 1) * 32;
-  static constexpr int kRows = 16 * MT;
-  static constexpr int kCtas = MT == 1 ? 2 : 1;     // a SM
+  static constexpr int kMK = kBK / 64;              // 16-key tiles a warp
+  static constexpr int kMD = D / 64;                // 16-column tiles of the output a warp
+  static constexpr int kRows = 8 * NR;
+  static constexpr int kCtas = NR <= 4 ? 2 : 1;     // a SM
+  static constexpr int kStages = NR <= 2 ? 3 : NR == 4 ? 2 : 4;  // what the shared memory holds
+  static constexpr bool kQRegs = NR * D <= 512;     // the queries' fragments stay in registers
   static constexpr int kHalfBytes = kBK * 128;      // 64 columns of a tile, one swizzle row a key
   static constexpr int kTileBytes = kBK * D * 2;    // K or V of a stage
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = MT == 1 ? 3 : MT == 2 ? 5 : 4;
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kQAt = kStages * kStageBytes;
   static constexpr int kPAt = kQAt + kStages * kQBytes;
-  static constexpr int kPBytes = kRows * kBK * 2;
-  static constexpr int kSmem = kPAt + 2 * kPBytes;  // weights by turns: a warp may be one tile ahead
+  static constexpr int kPBytes = NR * kBK * 16;     // weights [8-row tile][key][8 rows], bf16
+  static constexpr int kSmem = kPAt + 2 * kPBytes;  // by turns: a warp may be one tile ahead
 };
 
 constexpr int kRecFirst = 1, kRecLast = 2;  // of this CTA's part of the group
@@ -84,7 +84,7 @@ struct TileRec {
   int j0, n;          // first key of the tile, keys of the sequence
   int q;              // with `first`: which of the places holds the group's queries
   int flags;          // kRec...
-  int share, c0, c1;  // this share, and the shares that hold the group
+  int c0, c1;         // the shares that hold the group
   int slot, slot0;    // where this share's part lies, and where that of c0 does
   uint32_t bad[4];    // keys whose page is outside the cache
 };
@@ -137,14 +137,6 @@ __device__ __forceinline__ int share_of(long long x, int shares, long long total
   return p >> 32 ? (int)(p / total) : (int)((uint32_t)p / (uint32_t)total);
 }
 
-// Shares of a line of `total` tiles in `count` groups on `ctas` CTAs.
-__device__ __forceinline__ int share_count(long long total, long long count, int ctas) {
-  const long long least = (total + kMinTiles - 1) / kMinTiles;
-  if (least <= ctas) return (int)least;
-  if (count * 2 < ctas) return ctas;
-  return ctas * (int)min((long long)(kAttnShares / ctas), max(1ll, total / ((long long)ctas * kShareTiles)));
-}
-
 // Whether 16 bytes hold a bf16 infinity or NaN.
 __device__ __forceinline__ bool not_finite8(const uint4 &x) {
   const uint32_t e[4] = {x.x, x.y, x.z, x.w};
@@ -165,18 +157,19 @@ __device__ __forceinline__ bool win_meet(bool flag, int threads) {
   return any != 0;
 }
 
-template <int D, int MT>
-__global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
+template <int D, int NR>
+__global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
     attn_window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const __grid_constant__ WinArgs w) {
-  using C = WinCfg<D, MT>;
+  using C = WinCfg<D, NR>;
   constexpr int kChunks = D / 8;   // 16-byte pieces a row
-  constexpr int kNT = D / 64;      // 8-column tiles of a warp's output
   extern __shared__ __align__(1024) uint8_t win_smem[];
   __shared__ WinBars<C::kStages> B;
   __shared__ long long sum_s[C::kThreads / 32];
   __shared__ __align__(16) float row_s[C::kRows][C::kWarps];  // maxima, or sums, of each row by warp
-  __shared__ __align__(16) uint8_t use_s[2][16];  // by turns: a warp may be one tile ahead
+  __shared__ __align__(16) uint16_t use_s[2][8];  // by turns: a warp may be one tile ahead
+  __shared__ uint8_t tok_s[NR == 8 ? 1024 : C::kRows];  // the token of each row
+  __shared__ __align__(4) uint16_t mask_s[C::kWarps][C::kRows];  // keys of a warp's 16 that each row sees
   __shared__ int last_s;
   const AttnArgs &a = w.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -191,6 +184,8 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
     mbar_fence_init();
   }
 
+  for (int i = threadIdx.x; i < w.row_tiles * C::kRows; i += C::kThreads) tok_s[i] = (uint8_t)min(i / a.G, 255);
+
   // ---- the length of the line, and its shares
   if (blockIdx.x == 0) check_sequences(a.kv, a.T, a.status);
   long long total = 0;
@@ -203,137 +198,136 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
 #pragma unroll
   for (int i = 0; i < C::kThreads / 32; ++i) total += sum_s[i];
   total *= groups;
-  const int shares = share_count(total, (long long)a.kv.n_seqs * groups, gridDim.x);
-  if ((int)blockIdx.x >= shares) return;
+  const int shares = (int)min((long long)gridDim.x, total), share = blockIdx.x;
+  if (share >= shares) return;
 
   if (warp == C::kWarps) {
     // ---- producer: all but the pieces is uniform over the warp ----
     // lane l < pieces has piece l of a tile: a page, or half of one of 128
     const int log_pc = min(a.kv.log_ps, C::kLogBK), pc = 1 << log_pc, pieces = C::kBK >> log_pc;
-    int st = 0, qn = 0, b = 0, share = blockIdx.x;
+    int st = 0, qn = 0, b = 0;
     uint32_t ph = 1;
     long long issued = 0, line = 0;  // line: tiles before sequence b
-    bool live = true;
-    while (live && share < shares) {
-      // the next share, if there are more than CTAs: taken now, needed at this one's end
-      uint32_t claim = 0;
-      if (shares > (int)gridDim.x && lane == 0) claim = atomicAdd(a.counts + kAttnShares, 1u);
-      const long long x0 = mul_div(total, share, shares), x1 = mul_div(total, share + 1, shares);
-      // the sequence of x0: at or after the last share's
-      for (;;) {
-        long long incl = window_count(a, b + lane, C::kLogBK);
+    const long long x0 = mul_div(total, share, shares);
+    // the sequence of x0
+    for (;;) {
+      long long incl = window_count(a, b + lane, C::kLogBK);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += y;
-        }
-        const uint32_t beyond = __ballot_sync(0xffffffffu, line + incl * groups > x0);
-        const int at = beyond ? __ffs(beyond) - 1 : 32;
-        const long long skipped = __shfl_sync(0xffffffffu, incl, at > 0 ? at - 1 : 0);
-        if (at > 0) line += skipped * groups;
-        b += at;
-        if (beyond || b >= a.kv.n_seqs) break;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
       }
-      if (b >= a.kv.n_seqs) break;  // only where the lengths change under the call
-      SeqView s = seq_view(nullptr, a.kv.kv_len, b, a.kv.per, a.T, a.kv.cap);
-      TileRange r = window_tiles(a, s, C::kLogBK);
-      const int gi = (int)mul_div(x0 - line, 1, r.count);
-      int t = (int)(x0 - line - (long long)gi * r.count);
-      int hv = gi / w.row_tiles, rt = gi - hv * w.row_tiles;
-      // this lane's piece of the tile at the cursor
-      auto piece = [&](bool &seen) {
-        const int a0 = (tile_of(r, t) << C::kLogBK) + (lane << log_pc), e0 = a0 + pc;
-        seen = lane < pieces && a0 < s.n && (a.window <= 0 || e0 - 1 > s.n - s.m - a.window || a0 < a.n_sinks);
-        return seen ? __ldg(a.kv.table + (size_t)b * a.kv.max_pages + (a0 >> a.kv.log_ps)) : 0;
-      };
-      bool seen;
-      int page = piece(seen);
-      for (long long x = x0; x < x1; ++x) {
-        live = __all_sync(0xffffffffu, win_wait(&B.empty[st], ph, B, a.status));
-        if (!live) break;
-        const bool ok = seen && page >= 0 && page < a.kv.n_pages;
-        const uint32_t good = __ballot_sync(0xffffffffu, ok), wrong = __ballot_sync(0xffffffffu, seen && !ok);
-        const bool first = x == x0 || t == 0;
-        const int j0 = tile_of(r, t) << C::kLogBK, cb = b, chv = hv, crt = rt;
-        // below 2^31: checked on the host
-        const int row = ((page * a.V + hv) << a.kv.log_ps) + ((j0 + (lane << log_pc)) & ((1 << a.kv.log_ps) - 1));
-        if (lane == 0) {
-          TileRec &rec = B.rec[st];
-          const bool last = x + 1 == x1 || t + 1 == r.count;
-          rec.b = b;
-          rec.hv = hv;
-          rec.rt = rt;
-          rec.j0 = j0;
-          rec.n = s.n;
-          rec.q = qn;
-          rec.flags = (first ? kRecFirst : 0) | (last ? kRecLast : 0) |
-                      (wrong || !tile_full(s.n - s.m, s.n - 1, j0, C::kBK, s.n, a.window, a.n_sinks) ? kRecPartial : 0);
-          if (last) {
-            const long long gs = x - t, ge = gs + r.count;
-            rec.share = share;
-            rec.c0 = gs >= x0 ? share : share_of(gs, shares, total);
-            rec.c1 = ge <= x1 ? share : share_of(ge - 1, shares, total);
-            rec.slot = gs > x0;
-            rec.slot0 = gs > (gs >= x0 ? x0 : mul_div(total, rec.c0, shares));
-          }
-          rec.bad[0] = rec.bad[1] = rec.bad[2] = rec.bad[3] = 0;
-          if (wrong) {
-            for (int k = 0; k < C::kBK; ++k)
-              if (wrong >> (k >> log_pc) & 1) rec.bad[k >> 5] |= 1u << (k & 31);
-            set_status(a.status, kStatusBadIndex);
-          }
-          mbar_arrive_expect_tx(&B.full[st], (uint32_t)(__popc(good) * pc * D * 4));
+      const uint32_t beyond = __ballot_sync(0xffffffffu, line + incl * groups > x0);
+      const int at = beyond ? __ffs(beyond) - 1 : 32;
+      const long long skipped = __shfl_sync(0xffffffffu, incl, at > 0 ? at - 1 : 0);
+      if (at > 0) line += skipped * groups;
+      b += at;
+      if (beyond || b >= a.kv.n_seqs) break;
+    }
+    // (beyond the sequences, here or below, only where the lengths change under the call: no more tiles then)
+    long long x1 = b < a.kv.n_seqs ? mul_div(total, share + 1, shares) : x0;
+    b = min(b, a.kv.n_seqs - 1);
+    SeqView s = seq_view(nullptr, a.kv.kv_len, b, a.kv.per, a.T, a.kv.cap);
+    TileRange r = window_tiles(a, s, C::kLogBK);
+    const int gi = x1 > x0 ? (int)mul_div(x0 - line, 1, r.count) : 0;
+    int t = x1 > x0 ? (int)(x0 - line - (long long)gi * r.count) : 0;
+    int hv = gi / w.row_tiles, rt = gi - hv * w.row_tiles;
+    // this lane's piece of the tile at the cursor
+    auto piece = [&](bool &seen) {
+      const int a0 = (tile_of(r, t) << C::kLogBK) + (lane << log_pc), e0 = a0 + pc;
+      seen = lane < pieces && a0 < s.n && (a.window <= 0 || e0 - 1 > s.n - s.m - a.window || a0 < a.n_sinks);
+      return seen ? __ldg(a.kv.table + (size_t)b * a.kv.max_pages + (a0 >> a.kv.log_ps)) : 0;
+    };
+    bool seen;
+    int page = piece(seen);
+    for (long long x = x0; x < x1; ++x) {
+      if (!__all_sync(0xffffffffu, win_wait(&B.empty[st], ph, B, a.status))) break;
+      const bool ok = seen && page >= 0 && page < a.kv.n_pages;
+      const uint32_t good = __ballot_sync(0xffffffffu, ok), wrong = __ballot_sync(0xffffffffu, seen && !ok);
+      const bool first = x == x0 || t == 0;
+      const int j0 = tile_of(r, t) << C::kLogBK, cb = b, chv = hv, crt = rt;
+      // below 2^31: checked on the host
+      const int row = ((page * a.V + hv) << a.kv.log_ps) + ((j0 + (lane << log_pc)) & ((1 << a.kv.log_ps) - 1));
+      if (lane == 0) {
+        TileRec &rec = B.rec[st];
+        const bool last = x + 1 == x1 || t + 1 == r.count;
+        rec.b = b;
+        rec.hv = hv;
+        rec.rt = rt;
+        rec.j0 = j0;
+        rec.n = s.n;
+        rec.q = qn;
+        rec.flags = (first ? kRecFirst : 0) | (last ? kRecLast : 0) |
+                    (wrong || !tile_full(s.n - s.m, s.n - 1, j0, C::kBK, s.n, a.window, a.n_sinks) ? kRecPartial : 0);
+        if (last) {
+          const long long gs = x - t, ge = gs + r.count;
+          rec.c0 = gs >= x0 ? share : share_of(gs, shares, total);
+          rec.c1 = ge <= x1 ? share : share_of(ge - 1, shares, total);
+          rec.slot = gs > x0;
+          rec.slot0 = gs > (gs >= x0 ? x0 : mul_div(total, rec.c0, shares));
         }
-        __syncwarp();
-        if (ok) {
-          uint8_t *dst = win_smem + st * C::kStageBytes + lane * pc * 128;
+        rec.bad[0] = rec.bad[1] = rec.bad[2] = rec.bad[3] = 0;
+        if (wrong) {
+          for (int k = 0; k < C::kBK; ++k)
+            if (wrong >> (k >> log_pc) & 1) rec.bad[k >> 5] |= 1u << (k & 31);
+          set_status(a.status, kStatusBadIndex);
+        }
+        mbar_arrive_expect_tx(&B.full[st], (uint32_t)(__popc(good) * pc * D * 4));
+      }
+      __syncwarp();
+      // one elected lane issues all, on values that are uniform over the warp
+      constexpr int kPieces = C::kBK / 16;
+      int y[kPieces];
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            tma_load_2d(dst + h * C::kHalfBytes, &kmap, h * 64, row, &B.full[st]);
-            tma_load_2d(dst + C::kTileBytes + h * C::kHalfBytes, &vmap, h * 64, row, &B.full[st]);
+      for (int i = 0; i < kPieces; ++i) y[i] = __shfl_sync(0xffffffffu, row, i);
+      if (elect_one()) {
+        uint8_t *dst = win_smem + st * C::kStageBytes;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          if (good >> i & 1) {
+            uint8_t *d = dst + i * pc * 128;
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+              tma_load_2d(d + h * C::kHalfBytes, &kmap, h * 64, y[i], &B.full[st]);
+              tma_load_2d(d + C::kTileBytes + h * C::kHalfBytes, &vmap, h * 64, y[i], &B.full[st]);
+            }
           }
-        }
-        __syncwarp();
-        // the cursor, and the next tile's pages, which come in while this warp waits for a stage
-        if (++t == r.count) {
-          t = 0;
-          if (++rt == w.row_tiles) {
-            rt = 0;
-            if (++hv == a.V) {
-              hv = 0;
-              if (x + 1 < x1) {
-                line += (long long)r.count * groups;
-                s = seq_view(nullptr, a.kv.kv_len, ++b, a.kv.per, a.T, a.kv.cap);
-                r = window_tiles(a, s, C::kLogBK);
-              }
+      }
+      __syncwarp();
+      // the cursor, and the next tile's pages, which come in while this warp waits for a stage
+      if (++t == r.count) {
+        t = 0;
+        if (++rt == w.row_tiles) {
+          rt = 0;
+          if (++hv == a.V) {
+            hv = 0;
+            if (b + 1 == a.kv.n_seqs) x1 = x + 1;
+            if (x + 1 < x1) {
+              s = seq_view(nullptr, a.kv.kv_len, ++b, a.kv.per, a.T, a.kv.cap);
+              r = window_tiles(a, s, C::kLogBK);
             }
           }
         }
-        if (x + 1 < x1) page = piece(seen);
-        if (first) {
-          // the group's queries; rows behind the last are zeros.  The groups in flight are no more than the stages,
-          // so that as many places in turn suffice.
-          const uint32_t dst = smem0 + C::kQAt + (uint32_t)qn * C::kQBytes;
-          qn = qn + 1 == C::kStages ? 0 : qn + 1;
-          for (int i = lane; i < C::kRows * kChunks; i += 32) {
-            const int rr = i / kChunks, ch = i % kChunks, rg = crt * C::kRows + rr, tok = rg / a.G;
-            const bool in = rg < rows;
-            const uint16_t *src = a.q + (in ? (size_t)(cb * a.kv.per + tok) * a.ld_q + (size_t)(chv * a.G + rg - tok * a.G) * D + ch * 8 : 0);
-            cp_async16_or_zero(dst + (uint32_t)(rr * kChunks + (ch ^ (rr & 7))) * 16u, src, in);
-          }
-        }
-        cp_async_arrive(&B.full[st]);  // every lane, when its copies have landed
-        ++issued;
-        if (++st == C::kStages) {
-          st = 0;
-          ph ^= 1;
+      }
+      if (x + 1 < x1) page = piece(seen);
+      if (first) {
+        // the group's queries; rows behind the last are zeros.  The groups in flight are no more than the stages,
+        // so that as many places in turn suffice.
+        const uint32_t dst = smem0 + C::kQAt + (uint32_t)qn * C::kQBytes;
+        qn = qn + 1 == C::kStages ? 0 : qn + 1;
+        for (int i = lane; i < C::kRows * kChunks; i += 32) {
+          const int rr = i / kChunks, ch = i % kChunks, rg = crt * C::kRows + rr, tok = tok_s[rg];
+          const bool in = rg < rows;
+          const uint16_t *src = a.q + (in ? (size_t)(cb * a.kv.per + tok) * a.ld_q + (size_t)(chv * a.G + rg - tok * a.G) * D + ch * 8 : 0);
+          cp_async16_or_zero(dst + (uint32_t)(rr * kChunks + (ch ^ (rr & 7))) * 16u, src, in);
         }
       }
-      if (shares <= (int)gridDim.x) break;
-      claim = __shfl_sync(0xffffffffu, claim, 0);
-      share = gridDim.x + claim;
-      // every CTA makes one claim that finds nothing; the very last claim leaves the counter ready for the next call
-      if (lane == 0 && claim == (uint32_t)(shares - 1)) a.counts[kAttnShares] = 0;
+      cp_async_arrive(&B.full[st]);  // every lane, when its copies have landed
+      ++issued;
+      if (++st == C::kStages) {
+        st = 0;
+        ph ^= 1;
+      }
     }
     // The end record takes the oldest stage, whose tile has been read.
     const bool told = __all_sync(0xffffffffu, win_wait(&B.empty[st], ph, B, a.status));
@@ -356,66 +350,70 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
   constexpr int kMeet = C::kWarps * 32;
   uint32_t phase = 0;
   int cs = 0, turn = 0;
-  uint32_t qf[MT == 1 ? D / 16 : 1][4];  // a single row tile's queries stay in registers
-  float o[MT][kNT][4], m[MT][2], l[MT][2];
-  uint32_t qs = 0;                       // where the group's queries lie
+  uint32_t qf[C::kQRegs ? NR : 1][D / 16][2];
+  float o[C::kMD][NR][4], m[NR][2], l[NR][2];  // columns of the C fragment: rows 8 i + 2 c and one more
+  uint32_t qs = 0;                             // where the group's queries lie
+  // lane offsets in a stage: 16 keys x 2 pieces of K for ldmatrix, 16 keys x 2 pieces of V for its transposed form
+  const int kr = 16 * C::kMK * warp + (lane & 15), vr = (lane & 7) + ((lane >> 4) << 3);
+  const uint32_t koff = (uint32_t)(kr * 128 + (((lane >> 4) ^ (kr & 7)) << 4));
+  const uint32_t voff = (uint32_t)(C::kTileBytes + vr * 128);
   for (;;) {
     const bool came = win_wait(&B.full[cs], phase, B, a.status);
     const TileRec &rec = B.rec[cs];
     const int flags = came ? rec.flags : kRecEnd;
     const uint32_t st = smem0 + (uint32_t)cs * C::kStageBytes, ps = smem0 + C::kPAt + (uint32_t)turn * C::kPBytes;
-    float sc[MT][C::kNK][4];
+    float sc[C::kMK][NR][4];  // keys g and g + 8 of a tile, rows 2 c and 2 c + 1
     bool grow = flags & kRecEnd;
     if (!grow) {
       if (flags & kRecFirst) {
         qs = smem0 + C::kQAt + (uint32_t)rec.q * C::kQBytes;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
+        for (int i = 0; i < NR; ++i) {
 #pragma unroll
-          for (int t = 0; t < kNT; ++t) o[i][t][0] = o[i][t][1] = o[i][t][2] = o[i][t][3] = 0.f;
+          for (int t = 0; t < C::kMD; ++t) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
           m[i][0] = m[i][1] = -INFINITY;
           l[i][0] = l[i][1] = 0.f;
-        }
-        if constexpr (MT == 1) {
-          const int r = lane & 15;
+          if constexpr (C::kQRegs) {
+            const int r = 8 * i + (lane & 7);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            ldsm_x4(qs + (uint32_t)(r * kChunks + ((2 * k + (lane >> 4)) ^ (r & 7))) * 16u, qf[k][0], qf[k][1], qf[k][2],
-                    qf[k][3]);
+            for (int k = 0; k < D / 16; k += 2)
+              ldsm_x4(qs + (uint32_t)(r * kChunks + ((2 * k + (lane >> 3)) ^ (r & 7))) * 16u, qf[i][k][0], qf[i][k][1],
+                      qf[i][k + 1][0], qf[i][k + 1][1]);
+          }
         }
       }
       // ---- scores of this warp's keys
 #pragma unroll
-      for (int nk = 0; nk < C::kNK; ++nk) {
-        uint32_t kf[D / 16][2];
-        const int r = 8 * (C::kNK * warp + nk) + (lane & 7);
+      for (int t = 0; t < C::kMK; ++t) {
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          const int ch = 4 * k + (lane >> 3);
-          ldsm_x4(st + (uint32_t)((ch >> 3) * C::kHalfBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4)), kf[2 * k][0],
-                  kf[2 * k][1], kf[2 * k + 1][0], kf[2 * k + 1][1]);
-        }
+        for (int i = 0; i < NR; ++i) sc[t][i][0] = sc[t][i][1] = sc[t][i][2] = sc[t][i][3] = 0.f;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < D / 16; k += 2) {
+          uint32_t kf[2][4];
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            uint32_t af[4];
-            if constexpr (MT == 1) {
+          for (int e = 0; e < 2; ++e)
+            ldsm_x4((st + koff + (uint32_t)(t * 2048 + ((k + e) >> 2) * C::kHalfBytes)) ^ (uint32_t)(((k + e) & 3) << 5),
+                    kf[e][0], kf[e][1], kf[e][2], kf[e][3]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) af[e] = qf[k][e];
+          for (int i = 0; i < NR; ++i) {
+            uint32_t b[4];
+            if constexpr (C::kQRegs) {
+              b[0] = qf[i][k][0];
+              b[1] = qf[i][k][1];
+              b[2] = qf[i][k + 1][0];
+              b[3] = qf[i][k + 1][1];
             } else {
-              const int rq = 16 * i + (lane & 15);
-              ldsm_x4(qs + (uint32_t)(rq * kChunks + ((2 * k + (lane >> 4)) ^ (rq & 7))) * 16u, af[0], af[1], af[2], af[3]);
+              const int r = 8 * i + (lane & 7);
+              ldsm_x4(qs + (uint32_t)(r * kChunks + ((2 * k + (lane >> 3)) ^ (r & 7))) * 16u, b[0], b[1], b[2], b[3]);
             }
-            if (k & 1)
-              mma_bf16_16816(s1, af, kf[k][0], kf[k][1], s1);
-            else
-              mma_bf16_16816(s0, af, kf[k][0], kf[k][1], s0);
+            mma_bf16_16816(sc[t][i], kf[0], b[0], b[1], sc[t][i]);
+            mma_bf16_16816(sc[t][i], kf[1], b[2], b[3], sc[t][i]);
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[i][nk][e] = (s0[e] + s1[e]) * a.scale_log2;
         }
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[t][i][e] *= a.scale_log2;
       }
       if (flags & kRecPartial) {
         // which of the warp's keys some row sees, and of these the ones whose values are not finite: 0 * v is NaN
@@ -423,157 +421,160 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
         // see it become NaN
         const int n = rec.n, j0 = rec.j0, base_pos = n - a.kv.per, r0 = rec.rt * C::kRows;
 #pragma unroll
-        for (int nk = 0; nk < C::kNK; ++nk) {
-          const int k0 = 8 * (C::kNK * warp + nk), kk = k0 + (lane >> 2), j = j0 + kk;
+        for (int t = 0; t < C::kMK; ++t) {
+          // lane and lane + 16 look at one key, half of its values each
+          const int k0 = 16 * (C::kMK * warp + t), kk = k0 + (lane & 15), j = j0 + kk;
           const bool live = j < n && (a.window <= 0 || base_pos - j < a.window || j < a.n_sinks) &&
                             !(rec.bad[kk >> 5] >> (kk & 31) & 1);
           bool bad = false;
           if (live && a.kv.per > 1) {
             const uint8_t *v = win_smem + cs * C::kStageBytes + C::kTileBytes + kk * 128;
 #pragma unroll
-            for (int i = 0; i < kChunks / 4; ++i) {
-              const int ch = 4 * i + (lane & 3);
+            for (int i = 0; i < kChunks / 2; ++i) {
+              const int ch = (lane >> 4) * (kChunks / 2) + i;
               bad |= not_finite8(*reinterpret_cast<const uint4 *>(v + (ch >> 3) * C::kHalfBytes + (((ch & 7) ^ (kk & 7)) << 4)));
             }
           }
-          const uint32_t lv = __ballot_sync(0xffffffffu, live);
-          uint32_t bd = __ballot_sync(0xffffffffu, bad);  // a key's bits: lanes 4k .. 4k + 3
-          bd |= bd >> 1;
-          bd |= bd >> 2;
-          uint32_t use = 0;
+          const uint32_t lv = __ballot_sync(0xffffffffu, live) & 0xffffu;
+          uint32_t bd = __ballot_sync(0xffffffffu, bad);
+          bd = (bd | bd >> 16) & 0xffffu;
+          if (lane == 0) use_s[turn][C::kMK * warp + t] = (uint16_t)(lv & ~bd);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) use |= ((lv & ~bd) >> (4 * k) & 1) << k;
-          if (lane == 0) use_s[turn][C::kNK * warp + nk] = (uint8_t)use;
+          for (int r = lane; r < C::kRows; r += 32) {
+            const int hi = r0 + r < rows ? base_pos + tok_s[r0 + r] - (j0 + k0) : -1;  // keys up to hi,
+            const int lo = a.window > 0 ? hi - a.window + 1 : 0;                       // from lo on
+            const int sk = a.window > 0 ? a.n_sinks - (j0 + k0) : 0;                   // or below sk
+            mask_s[warp][r] = (uint16_t)(below(hi + 1) & (~below(lo) | below(sk)) & lv);
+          }
+          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
+          for (int i = 0; i < NR; ++i) {
+            // two rows' masks: this lane's keys are bits 0 and 8 of each after the shift
+            const uint32_t both = *reinterpret_cast<const uint32_t *>(&mask_s[warp][8 * i + 2 * c]), v = both >> g;
+            if (!(v & 1u)) sc[t][i][0] = -INFINITY;
+            if (!(v & 0x10000u)) sc[t][i][1] = -INFINITY;
+            if (!(v & 0x100u)) sc[t][i][2] = -INFINITY;
+            if (!(v & 0x1000000u)) sc[t][i][3] = -INFINITY;
+            if (bd) {
+              if (both & bd) l[i][0] = NAN;
+              if (both >> 16 & bd) l[i][1] = NAN;
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    // ---- weights, with the maximum as it stands; once more when one has to grow.  (A loop, so that its code is there
+    // once: a group's first tile always goes round twice.)
+    float sums[NR][2];
+    bool grown = false, out = false;
+    for (;;) {
+      if (!(flags & kRecEnd)) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int rg = r0 + 16 * i + g + 8 * h;
-              const int pos = rg < rows ? base_pos + rg / a.G : -1;
+        for (int i = 0; i < NR; ++i) {
+          if (grown) {
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int key = 2 * c + e;
-                const bool v = (lv >> (4 * key) & 1) && key_seen(pos, j0 + k0 + key, n, a.window, a.n_sinks);
-                if (v && (bd >> (4 * key) & 1)) l[i][h] = NAN;
-                if (!v) sc[i][nk][2 * h + e] = -INFINITY;
+            for (int e = 0; e < 2; ++e) {
+              const float4 x = *reinterpret_cast<const float4 *>(&row_s[8 * i + 2 * c + e][0]);
+              const float nm = fmaxf(m[i][e], fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)));
+              const float f = ex2(m[i][e] - (nm == -INFINITY ? 0.f : nm));
+              m[i][e] = nm;
+              l[i][e] *= f;
+#pragma unroll
+              for (int t = 0; t < C::kMD; ++t) {
+                o[t][i][e] *= f;
+                o[t][i][2 + e] *= f;
               }
             }
-        }
-      }
-    }
-    // ---- weights, with the maximum as it stands
-    auto weights = [&](int i, int h) {
-      const int r = 16 * i + g + 8 * h;
-      const float sub = m[i][h] == -INFINITY ? 0.f : m[i][h];  // nothing seen yet: 2^(-inf - 0) = 0
-      float sum = 0.f;
-#pragma unroll
-      for (int nk = 0; nk < C::kNK; ++nk) {
-        const float e0 = ex2(sc[i][nk][2 * h] - sub), e1 = ex2(sc[i][nk][2 * h + 1] - sub);
-        sum += e0 + e1;
-        const int ch = C::kNK * warp + nk;
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(ps + (uint32_t)(r * (2 * C::kBK) + ((ch ^ (r & 7)) << 4) + 4 * c)),
-                     "r"(pack_bf16x2(e0, e1))
-                     : "memory");
-      }
-      return sum;
-    };
-    float sums[MT][2];
-    if (!(flags & kRecEnd)) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float most = m[i][h] + kWinLazy;
-#pragma unroll
-          for (int nk = 0; nk < C::kNK; ++nk) grow |= !(sc[i][nk][2 * h] <= most) || !(sc[i][nk][2 * h + 1] <= most);
-          sums[i][h] = weights(i, h);
-        }
-    }
-    // the meeting: the weights are there, unless a maximum has to grow (or the end has come)
-    if (win_meet(grow, kMeet)) {
-      if (win_meet(!came, kMeet) || (flags & kRecEnd)) break;  // all leave together when a wait has given up
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float x = fmaxf(sc[i][0][2 * h], sc[i][0][2 * h + 1]);
-          if constexpr (C::kNK == 2) x = fmaxf(x, fmaxf(sc[i][C::kNK - 1][2 * h], sc[i][C::kNK - 1][2 * h + 1]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          if (c == 0) row_s[16 * i + g + 8 * h][warp] = x;
-        }
-      win_meet(false, kMeet);
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = 16 * i + g + 8 * h;
-          const float4 x0 = *reinterpret_cast<const float4 *>(&row_s[r][0]), x1 = *reinterpret_cast<const float4 *>(&row_s[r][4]);
-          const float mx = fmaxf(fmaxf(fmaxf(x0.x, x0.y), fmaxf(x0.z, x0.w)), fmaxf(fmaxf(x1.x, x1.y), fmaxf(x1.z, x1.w)));
-          const float nm = fmaxf(m[i][h], mx);
-          const float f = ex2(m[i][h] - (nm == -INFINITY ? 0.f : nm));
-          m[i][h] = nm;
-          l[i][h] *= f;
-#pragma unroll
-          for (int t = 0; t < kNT; ++t) {
-            o[i][t][2 * h] *= f;
-            o[i][t][2 * h + 1] *= f;
           }
-          sums[i][h] = weights(i, h);
+          // nothing seen yet: 2^(-inf - 0) = 0
+          const float s0 = m[i][0] == -INFINITY ? 0.f : m[i][0], s1 = m[i][1] == -INFINITY ? 0.f : m[i][1];
+          const float most0 = m[i][0] + kWinLazy, most1 = m[i][1] + kWinLazy;
+          float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+          for (int t = 0; t < C::kMK; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float x = sc[t][i][2 * h], y = sc[t][i][2 * h + 1];
+              grow |= !(x <= most0) || !(y <= most1);
+              const float e0 = ex2(x - s0), e1 = ex2(y - s1);
+              sum0 += e0;
+              sum1 += e1;
+              const int key = 16 * (C::kMK * warp + t) + g + 8 * h;
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(ps + (uint32_t)((i * C::kBK + key) * 16 + 4 * c)),
+                           "r"(pack_bf16x2(e0, e1))
+                           : "memory");
+            }
+          sums[i][0] = sum0;
+          sums[i][1] = sum1;
+        }
+      }
+      // the meeting: the weights are there, unless a maximum has to grow (or the end has come)
+      const bool again = win_meet(grow && !grown, kMeet);
+      if (!again) break;
+      out = win_meet(!came, kMeet) || (flags & kRecEnd);  // all leave together when a wait has given up
+      if (out) break;
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(sc[0][i][e], sc[0][i][2 + e]);
+          if constexpr (C::kMK == 2) x = fmaxf(x, fmaxf(sc[C::kMK - 1][i][e], sc[C::kMK - 1][i][2 + e]));
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+          if (g == 0) row_s[8 * i + 2 * c + e][warp] = x;
         }
       win_meet(false, kMeet);
+      grown = true;
     }
+    if (out) break;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
+    for (int i = 0; i < NR; ++i) {
       l[i][0] += sums[i][0];
       l[i][1] += sums[i][1];
     }
-    // ---- products: V fragments of this warp's columns, two 16-key steps a round
+    // ---- products over this warp's columns, two 16-key steps a round
 #pragma unroll
     for (int k = 0; k < C::kBK / 16; k += 2) {
-      uint32_t vf[2][kNT][2];
-      if constexpr (kNT == 2) {
+      uint32_t vf[2][C::kMD][4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 16 * (k + e) + (lane & 15), ch = 2 * warp + (lane >> 4);
-          ldsm_x4_t(st + (uint32_t)(C::kTileBytes + (ch >> 3) * C::kHalfBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
-                    vf[e][0][0], vf[e][0][1], vf[e][kNT - 1][0], vf[e][kNT - 1][1]);
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int t = 0; t < C::kMD; ++t) {
+          const int ch = 2 * (C::kMD * warp + t) + ((lane >> 3) & 1);
+          ldsm_x4_t(st + voff + (uint32_t)((k + e) * 2048 + (ch >> 3) * C::kHalfBytes + (((ch & 7) ^ (vr & 7)) << 4)),
+                    vf[e][t][0], vf[e][t][1], vf[e][t][2], vf[e][t][3]);
         }
-      } else {
-        const int r = 16 * k + lane;
-        ldsm_x4_t(st + (uint32_t)(C::kTileBytes + r * 128 + ((warp ^ (r & 7)) << 4)), vf[0][0][0], vf[0][0][1],
-                  vf[1][0][0], vf[1][0][1]);
-      }
       if (flags & kRecPartial) {
-        const uint32_t use = *reinterpret_cast<const volatile uint32_t *>(&use_s[turn][2 * k]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           // this lane's keys of the two halves of a fragment: 2c, 2c + 1 and 8 more
-          const uint32_t u = use >> (16 * e + 2 * c);
+          const uint32_t u = (uint32_t) * reinterpret_cast<const volatile uint16_t *>(&use_s[turn][k + e]) >> (2 * c);
           const uint32_t v0 = (u & 1 ? 0xffffu : 0u) | (u & 2 ? 0xffff0000u : 0u);
           const uint32_t v1 = (u & 256 ? 0xffffu : 0u) | (u & 512 ? 0xffff0000u : 0u);
 #pragma unroll
-          for (int t = 0; t < kNT; ++t) {
+          for (int t = 0; t < C::kMD; ++t) {
             vf[e][t][0] &= v0;
-            vf[e][t][1] &= v1;
+            vf[e][t][1] &= v0;
+            vf[e][t][2] &= v1;
+            vf[e][t][3] &= v1;
           }
         }
       }
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int i = 0; i < NR; ++i) {
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4_t(ps + (uint32_t)((i * C::kBK + 16 * k + lane) * 16), b0, b1, b2, b3);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 16 * i + (lane & 15);
-          uint32_t af[4];
-          ldsm_x4(ps + (uint32_t)(r * (2 * C::kBK) + (((2 * (k + e) + (lane >> 4)) ^ (r & 7)) << 4)), af[0], af[1], af[2], af[3]);
-#pragma unroll
-          for (int t = 0; t < kNT; ++t) mma_bf16_16816(o[i][t], af, vf[e][t][0], vf[e][t][1], o[i][t]);
+        for (int t = 0; t < C::kMD; ++t) {
+          mma_bf16_16816(o[t][i], vf[0][t], b0, b1, o[t][i]);
+          mma_bf16_16816(o[t][i], vf[1][t], b2, b3, o[t][i]);
         }
+      }
     }
     turn ^= 1;
-    int share = 0, c0 = 0, c1 = 0, slot = 0, slot0 = 0, hv = 0, q0 = 0, r0 = 0;
+    int c0 = 0, c1 = 0, slot = 0, slot0 = 0, hv = 0, q0 = 0, r0 = 0;
     if (flags & kRecLast) {
-      share = rec.share;
       c0 = rec.c0;
       c1 = rec.c1;
       slot = rec.slot;
@@ -592,38 +593,42 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
 
     // ---- the end of this CTA's part of the group: row sums over the warps, in warp order
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float x = l[i][h];
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        if (c == 0) row_s[16 * i + g + 8 * h][warp] = x;
+      for (int e = 0; e < 2; ++e) {
+        float x = l[i][e];
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+        if (g == 0) row_s[8 * i + 2 * c + e][warp] = x;
       }
     win_meet(false, kMeet);
     const int live = min(rows - r0, C::kRows);
     constexpr size_t kPart = (size_t)C::kRows * (D + 2);
     float *po = a.part + ((size_t)share * 2 + slot) * kPart, *pm = po + (size_t)C::kRows * D;
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 16 * i + g + 8 * h, rg = r0 + r, col = warp * (8 * kNT) + 2 * c;
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * i + 2 * c + e, col = 16 * C::kMD * warp + g;
         if (r >= live) continue;
-        const float4 x0 = *reinterpret_cast<const float4 *>(&row_s[r][0]), x1 = *reinterpret_cast<const float4 *>(&row_s[r][4]);
-        const float sum = ((x0.x + x0.y) + (x0.z + x0.w)) + ((x1.x + x1.y) + (x1.z + x1.w));
+        const float4 x = *reinterpret_cast<const float4 *>(&row_s[r][0]);
+        const float sum = (x.x + x.y) + (x.z + x.w);
         if (c0 == c1) {
           const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-          const int tok = rg / a.G;
+          const int rg = r0 + r, tok = tok_s[rg];
           uint16_t *dst = a.out + ((size_t)(q0 + tok) * a.H + (size_t)hv * a.G + rg - tok * a.G) * D + col;
 #pragma unroll
-          for (int t = 0; t < kNT; ++t)
-            *reinterpret_cast<uint32_t *>(dst + 8 * t) = pack_bf16x2(o[i][t][2 * h] * inv, o[i][t][2 * h + 1] * inv);
+          for (int t = 0; t < C::kMD; ++t) {
+            dst[16 * t] = float_to_bf16_bits(o[t][i][e] * inv);
+            dst[16 * t + 8] = float_to_bf16_bits(o[t][i][2 + e] * inv);
+          }
         } else {
 #pragma unroll
-          for (int t = 0; t < kNT; ++t)
-            __stcg(reinterpret_cast<float2 *>(po + (size_t)r * D + col + 8 * t), make_float2(o[i][t][2 * h], o[i][t][2 * h + 1]));
-          if (warp == 0 && c == 0) __stcg(reinterpret_cast<float2 *>(pm + 2 * r), make_float2(m[i][h], sum));
+          for (int t = 0; t < C::kMD; ++t) {
+            __stcg(po + (size_t)r * D + col + 16 * t, o[t][i][e]);
+            __stcg(po + (size_t)r * D + col + 16 * t + 8, o[t][i][2 + e]);
+          }
+          if (warp == 0 && g == 0) __stcg(reinterpret_cast<float2 *>(pm + 2 * r), make_float2(m[i][e], sum));
         }
       }
     if (c0 == c1) continue;
@@ -638,63 +643,81 @@ __global__ void __launch_bounds__(WinCfg<D, MT>::kThreads, WinCfg<D, MT>::kCtas)
     }
     win_meet(false, kMeet);
     if (!last_s) continue;
-    for (int i = threadIdx.x; i < live * (D / 2); i += kMeet) {
-      const int r = i / (D / 2), d = 2 * (i % (D / 2));
-      float mm = -INFINITY, ll = 0.f, y0 = 0.f, y1 = 0.f;
+    // two pieces of four columns a thread, with up to eight parts of both in flight
+    for (int i0 = threadIdx.x; i0 < live * (D / 4); i0 += 2 * kMeet) {
+      float mm[2] = {-INFINITY, -INFINITY}, ll[2] = {0.f, 0.f}, y[2][4] = {};
 #pragma unroll 1
       for (int e0 = c0; e0 <= c1; e0 += 8) {
-        float2 ml[8], v[8];  // eight parts in flight; behind the last one, the last with no weight
+        float2 ml[2][8];
+        float4 v[2][8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int k = min(e0 + e, c1);
+          const int k = min(e0 + e, c1);  // behind the last one, the last with no weight
           const float *pk = a.part + ((size_t)k * 2 + (k == c0 ? slot0 : 0)) * kPart;
-          ml[e] = __ldcg(reinterpret_cast<const float2 *>(pk + (size_t)C::kRows * D + 2 * r));
-          v[e] = __ldcg(reinterpret_cast<const float2 *>(pk + (size_t)r * D + d));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int i = min(i0 + u * kMeet, live * (D / 4) - 1);
+            ml[u][e] = __ldcg(reinterpret_cast<const float2 *>(pk + (size_t)C::kRows * D + 2 * (i / (D / 4))));
+            v[u][e] = __ldcg(reinterpret_cast<const float4 *>(pk + 4 * (size_t)i));
+          }
         }
-        float nm = mm;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) nm = fmaxf(nm, ml[e].x);
-        const float u = nm == -INFINITY ? 0.f : nm, f0 = ex2(mm - u);
-        mm = nm;
-        ll *= f0;
-        y0 *= f0;
-        y1 *= f0;
+        for (int u = 0; u < 2; ++u) {
+          float nm = mm[u];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (e0 + e > c1) continue;
-          const float f = ex2(ml[e].x - u);
-          ll += ml[e].y * f;
-          y0 += v[e].x * f;
-          y1 += v[e].y * f;
+          for (int e = 0; e < 8; ++e) nm = fmaxf(nm, ml[u][e].x);
+          const float sub = nm == -INFINITY ? 0.f : nm, f0 = ex2(mm[u] - sub);
+          mm[u] = nm;
+          ll[u] *= f0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[u][k] *= f0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (e0 + e > c1) continue;
+            const float f = ex2(ml[u][e].x - sub);
+            ll[u] += ml[u][e].y * f;
+            y[u][0] += v[u][e].x * f;
+            y[u][1] += v[u][e].y * f;
+            y[u][2] += v[u][e].z * f;
+            y[u][3] += v[u][e].w * f;
+          }
         }
       }
-      const float inv = ll == 0.f ? 0.f : 1.0f / ll;
-      const int rg = r0 + r, tok = rg / a.G;
-      uint16_t *dst = a.out + ((size_t)(q0 + tok) * a.H + (size_t)hv * a.G + rg - tok * a.G) * D + d;
-      *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(y0 * inv, y1 * inv);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = i0 + u * kMeet;
+        if (i >= live * (D / 4)) continue;
+        const float inv = ll[u] == 0.f ? 0.f : 1.0f / ll[u];
+        const int rg = r0 + i / (D / 4), tok = tok_s[rg];
+        uint16_t *dst = a.out + ((size_t)(q0 + tok) * a.H + (size_t)hv * a.G + rg - tok * a.G) * D + 4 * (i % (D / 4));
+        *reinterpret_cast<uint2 *>(dst) =
+            make_uint2(pack_bf16x2(y[u][0] * inv, y[u][1] * inv), pack_bf16x2(y[u][2] * inv, y[u][3] * inv));
+      }
     }
   }
 }
 
-template <int D, int MT>
+template <int D, int NR>
 cudaError_t launch(WinArgs w, const moe_kv_cache &c, cudaStream_t s) {
-  using C = WinCfg<D, MT>;
+  using C = WinCfg<D, NR>;
   CUtensorMap km, vm;
-  if (!make_pages_map(&km, c.k, c.n_pages, w.a, D, C::kBK) ||
-      !make_pages_map(&vm, c.v, c.n_pages, w.a, D, C::kBK))
+  if (!make_pages_map(&km, c.k, c.n_pages, w.a, D, C::kBK) || !make_pages_map(&vm, c.v, c.n_pages, w.a, D, C::kBK))
     return cudaErrorInvalidValue;
   w.row_tiles = (w.a.kv.per * w.a.G + C::kRows - 1) / C::kRows;
-  cudaError_t err = cudaFuncSetAttribute(attn_window_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  cudaError_t err = cudaFuncSetAttribute(attn_window_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (err != cudaSuccess) return err;
-  attn_window_kernel<D, MT><<<kAttnSms * C::kCtas, C::kThreads, C::kSmem, s>>>(km, vm, w);
+  attn_window_kernel<D, NR><<<kAttnSms * C::kCtas, C::kThreads, C::kSmem, s>>>(km, vm, w);
   return cudaGetLastError();
 }
 
-// Rows of a window: one, two or four 16-row tiles side by side; more rows than 64 walk the keys again.
+// Rows of a window: one, two, four or eight 8-row tiles side by side; more rows than 64 walk the keys again.
 template <int D>
 cudaError_t launch_d(const WinArgs &w, const moe_kv_cache &c, cudaStream_t s) {
   const int rows = w.a.kv.per * w.a.G;
-  return rows <= 16 ? launch<D, 1>(w, c, s) : rows <= 32 ? launch<D, 2>(w, c, s) : launch<D, 4>(w, c, s);
+  return rows <= 8    ? launch<D, 1>(w, c, s)
+         : rows <= 16 ? launch<D, 2>(w, c, s)
+         : rows <= 32 ? launch<D, 4>(w, c, s)
+                      : launch<D, 8>(w, c, s);
 }
 
 }  // namespace
@@ -713,7 +736,8 @@ bool make_pages_map(CUtensorMap *map, const uint16_t *cache, int n_pages, const 
 
 size_t attn_part_bytes(const moe_attn_dims &d, int, int) {
   const int rows = 8 * d.n_heads / d.n_kv_heads;  // the most rows of a window, then those of a CTA
-  return (size_t)kAttnShares * 2 * (rows <= 16 ? 16 : rows <= 32 ? 32 : 64) * (d.head_dim + 2) * 4;
+  // two parts a share; with more than 32 rows (one CTA a SM) there are half as many shares
+  return (size_t)kAttnShares * 2 * (rows <= 8 ? 8 : rows <= 16 ? 16 : 32) * (d.head_dim + 2) * 4;
 }
 
 cudaError_t launch_attn(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) {

@@ -22,7 +22,7 @@ cudaError_t launch_qk_norm_rope(const moe_attn_dims &d, const uint16_t *qkv, int
                                 const KvArgs &kv, int T, uint16_t *q_out, uint32_t *status, cudaStream_t s);
 
 constexpr int kAttnSms = 148;               // a window call has one or two CTAs a SM
-constexpr int kAttnShares = 4 * kAttnSms;   // the most shares into which its key tiles are cut
+constexpr int kAttnShares = 2 * kAttnSms;   // the most shares into which its key tiles are cut, one a CTA
 
 struct AttnArgs {
   const uint16_t *q;
@@ -35,7 +35,7 @@ struct AttnArgs {
   uint16_t *out;
   uint32_t *status;
   float *part;        // workspace: parts of split groups
-  uint32_t *counts;   // workspace header: parts that have come [kAttnShares], then shares taken; zero between calls
+  uint32_t *counts;   // workspace header: parts that have come, zero between calls [kAttnShares]
 };
 
 // One side of the cache as rows of D elements, boxes of a page's rows (at most `tile`) x 64 elements, 128-byte
@@ -60,6 +60,9 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// The lowest n bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),

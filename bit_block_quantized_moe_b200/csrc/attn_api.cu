@@ -14,9 +14,9 @@ static bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
 
 static moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
-constexpr size_t kWsHeader = 4096;  // the sticky status word; from byte 256 on the counts of parts
+constexpr size_t kWsHeader = 2048;  // the sticky status word; from byte 256 on the counts of parts
 constexpr size_t kWsCounts = 256;
-static_assert(kWsCounts + (kAttnShares + 1) * 4 <= kWsHeader, "the counts lie in the header");
+static_assert(kWsCounts + kAttnShares * 4 <= kWsHeader, "the counts lie in the header");
 
 static bool linear_dims_ok(int32_t T, int32_t K, int32_t N) {
   return T >= 0 && K >= 8 && K <= 65536 && K % 8 == 0 && N >= 1 && N <= 262144;

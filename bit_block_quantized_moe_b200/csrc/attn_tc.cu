@@ -80,9 +80,6 @@ __device__ __forceinline__ uint64_t sdesc_n_sw128(uint32_t addr, uint32_t group_
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// The lowest n bits (none for n <= 0, all for n >= 32).
-__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
-
 __device__ __forceinline__ float max_nan(float a, float b) {
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));

@@ -287,9 +287,9 @@ moe_status moe_rmsnorm_residual(float *resid, const uint16_t *y, uint16_t *x_nor
  *   moe_attn_forward    o = attention of q over the cache
  *   moe_linear          resid += o Wo^T
  *   moe_rmsnorm_residual(resid, NULL, x_norm), then the MoE half.
- * Calls are asynchronous, allocate nothing, and take a workspace.  Its first 4096
+ * Calls are asynchronous, allocate nothing, and take a workspace.  Its first 2048
  * bytes hold the sticky status word (read with moe_check_status) and counters that
- * every call leaves at zero: zero the workspace (or at least those 4096 bytes) once
+ * every call leaves at zero: zero the workspace (or at least those 2048 bytes) once
  * after allocating it, and again after a call reported MOE_ERR_TIMEOUT.  One
  * workspace must not be used by two calls that can run at the same time, two
  * captured graphs among them. */
