@@ -6,9 +6,13 @@
 // mod 2^64 loses whole turns and nothing else, so that the angle of position 2^30 is as exact as that of position 1
 // (an fp32 product position * frequency would be off by 0.03 radians at position 500,000).
 //
-// Bound: HBM (every element read once and written once).  A CTA takes kTok tokens: first its threads make the
-// tokens' sines and cosines (r/2 a token) in shared memory, then groups of D/8 lanes take a head row each, 16 bytes
-// a lane; the mean is a butterfly over the group, and a pair's partner is r/16 lanes away.
+// Bound: HBM (every element read once and written once), and close behind it the instructions.  Persistent CTAs take
+// kTok tokens a round.  Groups of D/16 lanes take a head row; a lane has two pieces of 8 elements, both partners of
+// its 8 pairs, so that the rotation needs no exchange and the mean a butterfly over few lanes.  All rows of a group
+// belong to one token, so that a lane keeps its sines and cosines in registers (made by the CTA's threads in shared
+// memory, r/2 a token); kDepth rows of the next step are in flight under the present one's arithmetic.  32768 tokens
+// of 20 heads: 151 us with one row in flight and the tables read per row, 113 us with five in flight and one piece of
+// 8 elements a lane, whose partner lay in another lane (185 instructions a piece).
 #include <algorithm>
 
 #include "attn.cuh"
@@ -17,7 +21,8 @@ namespace moe {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kTok = 4;  // tokens a CTA
+constexpr int kTok = 8;    // tokens a CTA, a warp's angles each
+constexpr int kDepth = 2;  // head rows in flight a lane
 
 struct NormArgs {
   const uint16_t *qkv;
@@ -31,27 +36,62 @@ struct NormArgs {
   uint32_t *status;
 };
 
+// (a0, a1) += (b0, b1) * (c0, c1), and (a0, a1) *= (b0, b1): one instruction for both, each lane rounded by itself.
+__device__ __forceinline__ void fma2(float &a0, float &a1, float b0, float b1, float c0, float c1) {
+  uint64_t acc, b, c;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(acc) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(c0), "f"(c1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(b), "l"(c));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(acc));
+}
+__device__ __forceinline__ void mul2(float &a0, float &a1, float b0, float b1) {
+  uint64_t acc, b;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(acc) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(b));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(acc));
+}
+
 template <int D>
-__global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const __grid_constant__ NormArgs a,
-                                                                    const __grid_constant__ moe_rope rope) {
-  constexpr int kGroup = D / 8;                  // lanes a head row
-  constexpr int kRows = kNormThreads / kGroup;   // head rows a pass of the CTA
-  __shared__ float2 cs[kTok][64];
-  __shared__ int pos_s[kTok];
-  __shared__ int64_t row_s[kTok];
-  const int t0 = blockIdx.x * kTok;
+__global__ void __launch_bounds__(kNormThreads, 2) qk_norm_rope_kernel(const __grid_constant__ NormArgs a,
+                                                                       const __grid_constant__ moe_rope rope) {
+  constexpr int kGroup = D / 16;                         // lanes a head row
+  constexpr int kStep = kNormThreads / kGroup / kTok;    // groups a token
+  static_assert(kNormThreads / 32 == kTok, "a warp makes a token's angles");
+  __shared__ float2 cs[2][kTok][64];
+  __shared__ int pos_s[2][kTok];
+  __shared__ int64_t row_s[2][kTok];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0) check_sequences(a.kv, a.T, a.status);
-  if (warp < kTok) {
-    const int t = t0 + warp;
+  const int group = threadIdx.x / kGroup, sub = threadIdx.x % kGroup;
+  const int tt = group / kStep, h0 = group % kStep;
+  const int heads = a.H + 2 * a.V, steps = (heads + kDepth * kStep - 1) / (kDepth * kStep);
+  // this lane's pieces: elements e0 .. e0 + 7 and e1 .. e1 + 7, partners where they are turned
+  const bool turned = sub * 8 < a.half;
+  const int e0 = turned ? sub * 8 : sub * 16, e1 = turned ? a.half + sub * 8 : sub * 16 + 8;
+  auto fetch = [&](int t0, int step, uint4 (&r)[kDepth][2]) {
+    const int t = t0 + tt;
+    const uint16_t *src = a.qkv + (size_t)min(t, a.T - 1) * a.ld;
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) {
+      const int h = h0 + (step * kDepth + i) * kStep;
+      const bool in = t < a.T && h < heads;
+      r[i][0] = in ? ldg_nc_v4(src + (size_t)h * D + e0) : make_uint4(0, 0, 0, 0);
+      r[i][1] = in ? ldg_nc_v4(src + (size_t)h * D + e1) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  // a token's position, cache row and angles, by a warp, two angles a lane
+  const uint64_t turn0 = rope.turn[lane], turn1 = rope.turn[lane + 32];
+  auto tables = [&](int t0, int par) {
+    const int tw = t0 + warp;
     int pos = INT_MIN;  // no sequence's row
     int64_t row = -1;
-    if (t < a.T) {
-      const int b = seq_of_row(a.kv, t, lane);
+    if (tw < a.T) {
+      const int b = seq_of_row(a.kv, tw, lane);
       if (b >= 0) {
         const SeqView s = seq_view(a.kv.q_start, a.kv.kv_len, b, a.kv.per, a.T, a.kv.cap);
-        if (t >= s.q0 && t < s.q0 + s.m) {
-          pos = s.n - s.m + (t - s.q0);
+        if (tw >= s.q0 && tw < s.q0 + s.m) {
+          pos = s.n - s.m + (tw - s.q0);
           if (pos >= 0) {
             row = cache_row(a.kv.table + (size_t)b * a.kv.max_pages, pos, a.kv.log_ps, a.kv.n_pages, a.V);
             if (row < 0 && lane == 0) set_status(a.status, kStatusBadIndex);
@@ -60,75 +100,109 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const __grid
       }
     }
     if (lane == 0) {
-      pos_s[warp] = pos;
-      row_s[warp] = row;
+      pos_s[par][warp] = pos;
+      row_s[par][warp] = row;
     }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < kTok * a.half; i += kNormThreads) {
-    const int t = i / a.half, e = i - t * a.half;
-    const int pos = pos_s[t];
-    if (pos >= 0) {
-      const int64_t turns = (int64_t)((uint64_t)pos * rope.turn[e]);  // signed: half a turn each way
-      // 2^-63 of the signed fraction is the angle in half turns, which sincospi takes exactly
-      float s, c;
-      sincospif((float)((double)turns * 0x1p-63), &s, &c);
-      cs[t][e] = make_float2(c, s);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (lane + 32 * e >= a.half) break;
+      const int64_t turns = (int64_t)((uint64_t)max(pos, 0) * (e ? turn1 : turn0));  // signed: half a turn each way
+      // the angle within half a turn: there the fast sine and cosine are good to 2^-20, far below bf16's step
+      float sn, cn;
+      __sincosf((float)turns * (0x1p-63f * 3.14159265358979f), &sn, &cn);
+      cs[par][warp][lane + 32 * e] = make_float2(cn, sn);
     }
+  };
+  float gq[16], gk[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int e = k < 8 ? e0 + k : e1 + k - 8;
+    gq[k] = a.gq ? __ldg(a.gq + e) : 1.f;
+    gk[k] = a.gk ? __ldg(a.gk + e) : 1.f;
   }
-  __syncthreads();
-
-  const int heads = a.H + 2 * a.V;
-  const int sub = threadIdx.x % kGroup;
-  const int e0 = sub * 8;               // this lane's elements
-  const int part = a.half / 8;          // lanes to a pair's partner
-  const bool turned = e0 < 2 * a.half, upper = e0 >= a.half;
-  const int freq0 = upper ? e0 - a.half : e0;
-  const int total = kTok * heads;
-  const int rounds = (total + kRows - 1) / kRows;
-  for (int it = 0; it < rounds; ++it) {
-    const int rr = it * kRows + threadIdx.x / kGroup;
-    const int tt = rr / heads, h = rr - tt * heads;
-    const int t = t0 + tt;
-    const int pos = rr < total ? pos_s[tt] : INT_MIN;
-    const bool live = rr < total && t < a.T && pos != INT_MIN;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (live) raw = ldg_nc_v4(a.qkv + (size_t)t * a.ld + (size_t)h * D + e0);
-    float x[8];
-    unpack8(raw, x);
-    float ss = 0.f;
+  uint4 raw[kDepth][2];
+  int t0 = blockIdx.x * kTok, par = 0;
+  fetch(t0, 0, raw);
+  tables(t0, 0);
+  for (; t0 < a.T; t0 += gridDim.x * kTok, par ^= 1) {
+    // the tables of two rounds stand by turns: one meeting a round, the next round's made before it
+    __syncthreads();
+    tables(t0 + gridDim.x * kTok, par ^ 1);
+    const int t = t0 + tt, pos = pos_s[par][tt];
+    const int64_t row = row_s[par][tt];
+    const bool live = t < a.T && pos != INT_MIN;
+    float cn[8], sn[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+    for (int i = 0; i < 8; ++i) {
+      const float2 w = turned ? cs[par][tt][e0 + i] : make_float2(1.f, 0.f);
+      cn[i] = w.x;
+      sn[i] = w.y;
+    }
+    for (int step = 0; step < steps; ++step) {
+      uint4 next[kDepth][2];
+      if (step + 1 < steps)
+        fetch(t0, step + 1, next);
+      else
+        fetch(t0 + gridDim.x * kTok, 0, next);
 #pragma unroll
-    for (int o = kGroup / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-    const float *gain = h < a.H ? a.gq : a.gk;
+      for (int i = 0; i < kDepth; ++i) {
+        const int h = h0 + (step * kDepth + i) * kStep;
+        if ((step * kDepth + i) * kStep >= heads) break;  // no group of the token has a row left
+        if (h >= a.H + a.V) {  // a value head: as it is
+          if (live && h < heads && row >= 0) {
+            uint16_t *dst = a.v + ((size_t)row + ((size_t)(h - a.H - a.V) << a.kv.log_ps)) * D;
+            *reinterpret_cast<uint4 *>(dst + e0) = raw[i][0];
+            *reinterpret_cast<uint4 *>(dst + e1) = raw[i][1];
+          }
+          continue;
+        }
+        float x[8], y[8];
+        unpack8(raw[i][0], x);
+        unpack8(raw[i][1], y);
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * (gain ? __ldg(gain + e0 + i) : 1.0f);
-    if (a.half) {
-      // every lane takes part in the exchange; those beyond the rotated part read a lane of their own group
-      const int from = turned ? (upper ? lane - part : lane + part) : lane;
+        for (int k = 0; k < 8; ++k) fma2(s0, s1, x[k], y[k], x[k], y[k]);
+        float ss = s0 + s1;
+        const uint32_t lanes = ((1u << kGroup) - 1u) << (lane & ~(kGroup - 1));  // this group's: its rows are of one kind
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = __shfl_sync(0xffffffffu, x[i], from);
-        if (live && turned && pos >= 0) {
-          const float2 w = cs[tt][freq0 + i];
-          x[i] = upper ? fmaf(x[i], w.x, y * w.y) : fmaf(x[i], w.x, -(y * w.y));
+        for (int o = kGroup / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(lanes, ss, o);
+        const float inv = rsqrtf(ss * (1.0f / D) + a.eps);  // within 2 units of the last place: far below bf16's step
+        const bool is_q = h < a.H;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          mul2(x[k], y[k], inv, inv);
+          mul2(x[k], y[k], is_q ? gq[k] : gk[k], is_q ? gq[k + 8] : gk[k + 8]);
+        }
+        if (turned) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            // (x, y) (c, c) + (-y, x) (s, s)
+            float u = -y[k] * sn[k], v = x[k] * sn[k];
+            fma2(u, v, x[k], y[k], cn[k], cn[k]);
+            x[k] = u;
+            y[k] = v;
+          }
+        }
+        if (!live) continue;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        if (is_q) {
+          uint16_t *dst = a.q_out + ((size_t)t * a.H + h) * D;
+          *reinterpret_cast<uint4 *>(dst + e0) = pos < 0 ? zero : pack8(x);
+          *reinterpret_cast<uint4 *>(dst + e1) = pos < 0 ? zero : pack8(y);
+        } else if (row >= 0) {
+          uint16_t *dst = a.k + ((size_t)row + ((size_t)(h - a.H) << a.kv.log_ps)) * D;
+          *reinterpret_cast<uint4 *>(dst + e0) = pack8(x);
+          *reinterpret_cast<uint4 *>(dst + e1) = pack8(y);
         }
       }
-    }
-    if (!live) continue;
-    if (h < a.H) {
-      uint4 o = pack8(x);
-      if (pos < 0) o = make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4 *>(a.q_out + ((size_t)t * a.H + h) * D + e0) = o;
-    } else if (row_s[tt] >= 0) {
-      const bool is_k = h < a.H + a.V;
-      const int hv = is_k ? h - a.H : h - a.H - a.V;
-      uint16_t *dst = (is_k ? a.k : a.v) + ((size_t)row_s[tt] + ((size_t)hv << a.kv.log_ps)) * D + e0;
-      *reinterpret_cast<uint4 *>(dst) = is_k ? pack8(x) : raw;
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i) {
+        raw[i][0] = next[i][0];
+        raw[i][1] = next[i][1];
+      }
     }
   }
+  if (blockIdx.x == 0) check_sequences(a.kv, a.T, a.status);
 }
 
 }  // namespace
@@ -140,7 +214,7 @@ cudaError_t launch_qk_norm_rope(const moe_attn_dims &d, const uint16_t *qkv, int
              status};
   moe_rope none{};
   const moe_rope &r = rope ? *rope : none;
-  const unsigned grid = (unsigned)((T + kTok - 1) / kTok);
+  const unsigned grid = (unsigned)std::min((T + kTok - 1) / kTok, 2 * 148);  // two CTAs a SM
   trace_mark(MOE_KERNEL_QK_NORM, false, s);
   if (d.head_dim == 128)
     qk_norm_rope_kernel<128><<<grid, kNormThreads, 0, s>>>(a, r);
