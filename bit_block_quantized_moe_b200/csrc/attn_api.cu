@@ -66,7 +66,7 @@ extern "C" {
 
 size_t moe_linear_workspace_bytes(int32_t max_T, int32_t K, int32_t N) {
   if (!linear_dims_ok(max_T, K, N)) return 0;
-  return kWsHeader + linear_part_bytes();
+  return kWsHeader;
 }
 
 moe_status moe_linear(const uint16_t *x, int64_t ld_x, const uint16_t *w, const float *bias, moe_act act,
@@ -87,9 +87,7 @@ moe_status moe_linear(const uint16_t *x, int64_t ld_x, const uint16_t *w, const 
   if (ws_bytes < moe_linear_workspace_bytes(T, K, N)) return MOE_ERR_WORKSPACE;
   const moe_status dev = device_ok();
   if (dev != MOE_OK) return dev;
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
-  return cuda_status(launch_linear(x, ld_x, w, bias, act, resid, out, T, K, N,
-                                   reinterpret_cast<float *>(ws + kWsHeader), reinterpret_cast<uint32_t *>(ws),
+  return cuda_status(launch_linear(x, ld_x, w, bias, act, resid, out, T, K, N, static_cast<uint32_t *>(workspace),
                                    reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -88,10 +88,8 @@ cudaError_t launch_combine_rmsnorm(const moe_dims &d, int T, const Workspace &ws
 constexpr int kHostIoMaxTokens = 8;
 cudaError_t launch_stream_copy16(const void *src, void *dst, size_t bytes, cudaStream_t s);
 void *mapped_host_range(const void *p, size_t bytes);
-// Matrix product with its epilogue (linear.cu); `part` holds linear_part_bytes() for the K-split parts.
-size_t linear_part_bytes();
+// Matrix product with its epilogue (linear.cu).
 cudaError_t launch_linear(const uint16_t *x, int64_t ld, const uint16_t *w, const float *bias, int act,
-                          const float *resid, void *out, int T, int K, int N, float *part, uint32_t *status,
-                          cudaStream_t s);
+                          const float *resid, void *out, int T, int K, int N, uint32_t *status, cudaStream_t s);
 
 }  // namespace moe

@@ -10,8 +10,9 @@
 //   epilogue warps : tensor memory lane quadrant = warp & 3; with 8 of them each has half of the columns.
 // With an fp32 output K runs in slices of 256: each slice has a fresh accumulator, added in fp32 to a running sum in
 // the epilogue's registers, because the tensor core's long accumulation truncates and loses up to 4e-6 of the result
-// at K = 2048, which bf16 hides and fp32 does not.  When the tiles alone leave SMs idle, K is also split over CTAs
-// and a second kernel adds the parts in split order.  Every wait is bounded (sync.cuh).
+// at K = 2048, which bf16 hides and fp32 does not.  When the tiles alone leave SMs idle, a cluster of 2, 4 or 8 CTAs
+// splits K: each sends the others their features' parts through distributed shared memory and finishes its own,
+// summed in rank order.  Every wait is bounded (sync.cuh).
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -25,7 +26,8 @@ constexpr int kLnK = 64;          // K a chunk: one 128-byte swizzle row
 constexpr int kLnSliceChunks = 4;  // chunks a slice, fp32 output
 constexpr int kLnWave = 148;
 
-template <int BN>
+// SPLIT: clusters share K, a tile a CTA.  Otherwise persistent CTAs.
+template <int BN, bool SPLIT>
 struct LnCfg {
   static constexpr int kEpiWarps = BN >= 128 ? 8 : 4;
   static constexpr int kThreads = (2 + kEpiWarps) * 32;
@@ -33,14 +35,17 @@ struct LnCfg {
   static constexpr int kABytes = kLnM * kLnK * 2;
   static constexpr int kBBytes = BN * kLnK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = 196608 / kStageBytes > 8 ? 8 : 196608 / kStageBytes;
+  static constexpr int kStages = SPLIT ? (BN >= 128 ? 4 : BN == 64 ? 5 : 4) : BN == 256 ? 4 : 6;
+  static constexpr int kSumBytes = SPLIT ? kLnM * BN * 4 : 0;  // the cluster's parts of this CTA's features
   static constexpr uint32_t kTmemCols = 2 * BN;
+  static constexpr int kSumAt = kStages * kStageBytes;
+  static constexpr int kBarsAt = kSumAt + kSumBytes;
   static_assert(kStageBytes % 1024 == 0, "stages keep the 1024-byte alignment of the 128-byte swizzle");
 };
 
-template <int BN>
+template <int STAGES>
 struct LnBars {
-  uint64_t full[LnCfg<BN>::kStages], empty[LnCfg<BN>::kStages], dfull[2], dempty[2], done;
+  uint64_t full[STAGES], empty[STAGES], dfull[2], dempty[2], done;
   uint32_t tmem;
   int abort;
 };
@@ -52,7 +57,6 @@ struct LnArgs {
   int act;
   const float *bias, *resid;
   void *out;
-  float *part;  // [ks][T][N], ks > 1
   uint32_t *status;
 };
 
@@ -68,27 +72,66 @@ __device__ __forceinline__ bool ln_wait(uint64_t *bar, uint32_t parity, Bars &B,
   return true;
 }
 
-__device__ __forceinline__ float ln_act(float z, int act) {
-  if (act == MOE_ACT_SILU) return z / (1.0f + __expf(-z));
-  if (act == MOE_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-  return z;
+// Finishes COUNT outputs i0, i0 + step, ... of sums z (with the bias in them), those with ok set: residuals are read
+// together, before the first store, which may go to the same memory.
+template <int COUNT>
+__device__ __forceinline__ void ln_finish(const LnArgs &a, size_t i0, size_t step, float (&z)[COUNT], int ok) {
+  if (a.act == MOE_ACT_SILU) {
+#pragma unroll
+    for (int n = 0; n < COUNT; ++n) z[n] = z[n] / (1.0f + __expf(-z[n]));
+  } else if (a.act == MOE_ACT_GELU) {
+#pragma unroll
+    for (int n = 0; n < COUNT; ++n) z[n] = 0.5f * z[n] * (1.0f + erff(z[n] * 0.70710678118654752f));
+  }
+  if (a.resid) {
+    float r[COUNT];
+#pragma unroll
+    for (int n = 0; n < COUNT; ++n) r[n] = n < ok ? a.resid[i0 + n * step] : 0.f;
+#pragma unroll
+    for (int n = 0; n < COUNT; ++n)
+      if (n < ok) static_cast<float *>(a.out)[i0 + n * step] = r[n] + z[n];
+  } else {
+#pragma unroll
+    for (int n = 0; n < COUNT; ++n)
+      if (n < ok) static_cast<uint16_t *>(a.out)[i0 + n * step] = float_to_bf16_bits(z[n]);
+  }
 }
 
-__device__ __forceinline__ void ln_store(const LnArgs &a, size_t i, float z) {
-  z = ln_act(z, a.act);
-  if (a.resid)
-    static_cast<float *>(a.out)[i] = a.resid[i] + z;
-  else
-    static_cast<uint16_t *>(a.out)[i] = float_to_bf16_bits(z);
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The address of this CTA's shared address in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_store(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int BN>
-__global__ void __launch_bounds__(LnCfg<BN>::kThreads, 1)
+// Sends COUNT tokens' sums of feature f of the tile, from token t0 of the tile on, to the rank that finishes the
+// feature: [rank][token][feature of that rank].
+template <int BN, int COUNT>
+__device__ __forceinline__ void ln_send(uint8_t *sums, int ks, int f, int t0, const float (&z)[COUNT]) {
+  const int own = kLnM / ks, to = f / own;
+  const uint32_t at = cluster_map(smem_u32(sums), to) + (uint32_t)((cluster_rank() * BN + t0) * own + f - to * own) * 4u;
+#pragma unroll
+  for (int n = 0; n < COUNT; ++n) cluster_store(at + (uint32_t)(n * own) * 4u, z[n]);
+}
+
+template <int BN, bool SPLIT>
+__global__ void __launch_bounds__(LnCfg<BN, SPLIT>::kThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, LnArgs a) {
-  using C = LnCfg<BN>;
+  using C = LnCfg<BN, SPLIT>;
   extern __shared__ __align__(1024) uint8_t ln_raw[];
   uint8_t *smem = ln_raw + ((1024u - (smem_u32(ln_raw) & 1023u)) & 1023u);
-  LnBars<BN> &B = *reinterpret_cast<LnBars<BN> *>(smem + C::kStages * C::kStageBytes);
+  LnBars<C::kStages> &B = *reinterpret_cast<LnBars<C::kStages> *>(smem + C::kBarsAt);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -106,6 +149,7 @@ __global__ void __launch_bounds__(LnCfg<BN>::kThreads, 1)
   }
   if (warp == 0) tmem_alloc(&B.tmem, C::kTmemCols);
   tc_fence_before();
+  if constexpr (SPLIT) cluster_meet();  // every CTA of the cluster is there before its memory is written
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = B.tmem;
@@ -181,43 +225,84 @@ __global__ void __launch_bounds__(LnCfg<BN>::kThreads, 1)
       const int ks = u % a.ks, tile = u / a.ks, ft = tile % a.n_ft, tt = tile / a.n_ft;
       const int c1 = (int)((long long)a.chunks * (ks + 1) / a.ks);
       int c = (int)((long long)a.chunks * ks / a.ks);
-      float run[C::kCols];
-#pragma unroll
-      for (int n = 0; n < C::kCols; ++n) run[n] = 0.f;
-      for (; c < c1; c += a.slice, ++sc) {
-        const int db = sc & 1;
-        ln_wait(&B.dfull[db], (sc >> 1) & 1, B, a.status);
+      const int f = ft * kLnM + 32 * q + lane, t0 = tt * BN + part * C::kCols;
+      const float b = a.bias && f < a.N ? a.bias[f] : 0.f;
+      if (!SPLIT && BN == 256 || c + a.slice >= c1) {
+        // one slice: straight out of tensor memory, a group of columns at a time
+        ln_wait(&B.dfull[sc & 1], (sc >> 1) & 1, B, a.status);
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < C::kCols; h += kStep) {
           uint32_t v[32];
           if constexpr (kStep == 32)
-            tmem_ld_32x32b_x32(tcol + db * BN + h, v);
+            tmem_ld_32x32b_x32(tcol + (sc & 1) * BN + h, v);
           else
-            tmem_ld_32x32b_x16(tcol + db * BN + h, v);
+            tmem_ld_32x32b_x16(tcol + (sc & 1) * BN + h, v);
           tmem_wait_ld();
+          float z[kStep];
 #pragma unroll
-          for (int n = 0; n < kStep; ++n) run[h + n] += __uint_as_float(v[n]);
+          for (int n = 0; n < kStep; ++n) z[n] = __uint_as_float(v[n]);
+          if constexpr (SPLIT) {
+            ln_send<BN>(smem + C::kSumAt, a.ks, 32 * q + lane, part * C::kCols + h, z);
+          } else {
+#pragma unroll
+            for (int n = 0; n < kStep; ++n) z[n] += b;
+            if (f < a.N) ln_finish(a, (size_t)(t0 + h) * a.N + f, (size_t)a.N, z, a.T - t0 - h);
+          }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B.dempty[db]);
-      }
-      const int f = ft * kLnM + 32 * q + lane;
-      if (f < a.N) {
-        const int t0 = tt * BN + part * C::kCols;
-        if (a.ks > 1) {
-          float *o = a.part + (size_t)ks * a.T * a.N;
+        if (lane == 0) mbar_arrive(&B.dempty[sc & 1]);
+        ++sc;
+      } else if constexpr (BN <= 128) {
+        float run[C::kCols];
 #pragma unroll
-          for (int n = 0; n < C::kCols; ++n)
-            if (t0 + n < a.T) o[(size_t)(t0 + n) * a.N + f] = run[n];
-        } else {
-          const float b = a.bias ? a.bias[f] : 0.f;
+        for (int n = 0; n < C::kCols; ++n) run[n] = SPLIT ? 0.f : b;
+        for (; c < c1; c += a.slice, ++sc) {
+          const int db = sc & 1;
+          ln_wait(&B.dfull[db], (sc >> 1) & 1, B, a.status);
+          tc_fence_after();
 #pragma unroll
-          for (int n = 0; n < C::kCols; ++n)
-            if (t0 + n < a.T) ln_store(a, (size_t)(t0 + n) * a.N + f, run[n] + b);
+          for (int h = 0; h < C::kCols; h += kStep) {
+            uint32_t v[32];
+            if constexpr (kStep == 32)
+              tmem_ld_32x32b_x32(tcol + db * BN + h, v);
+            else
+              tmem_ld_32x32b_x16(tcol + db * BN + h, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int n = 0; n < kStep; ++n) run[h + n] += __uint_as_float(v[n]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&B.dempty[db]);
+        }
+#pragma unroll
+        for (int h = 0; h < C::kCols; h += kStep) {
+          float z[kStep];
+#pragma unroll
+          for (int n = 0; n < kStep; ++n) z[n] = run[h + n];
+          if constexpr (SPLIT)
+            ln_send<BN>(smem + C::kSumAt, a.ks, 32 * q + lane, part * C::kCols + h, z);
+          else if (f < a.N)
+            ln_finish(a, (size_t)(t0 + h) * a.N + f, (size_t)a.N, z, a.T - t0 - h);
         }
       }
+    }
+  }
+  if constexpr (SPLIT) {
+    __syncwarp();
+    cluster_meet();  // the parts are there
+    // this CTA's features, the ranks' parts in rank order
+    const int tile = blockIdx.x / a.ks, ft = tile % a.n_ft, tt = tile / a.n_ft, own = kLnM / a.ks;
+    const float *sums = reinterpret_cast<const float *>(smem + C::kSumAt);
+    const int f0 = ft * kLnM + (int)cluster_rank() * own;
+    for (int i = threadIdx.x; i < own * BN; i += C::kThreads) {
+      const int f = f0 + i % own, t = tt * BN + i / own;
+      if (f >= a.N || t >= a.T) continue;
+      float z[1] = {a.bias ? a.bias[f] : 0.f};
+      for (int r = 0; r < a.ks; ++r) z[0] += sums[r * own * BN + i];
+      ln_finish(a, (size_t)t * a.N + f, 0, z, 1);
     }
   }
   tc_fence_before();
@@ -225,16 +310,6 @@ __global__ void __launch_bounds__(LnCfg<BN>::kThreads, 1)
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tbase, C::kTmemCols);
-  }
-}
-
-// The parts in split order, then the epilogue.
-__global__ void linear_join_kernel(LnArgs a) {
-  const size_t n = (size_t)a.T * a.N;
-  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) {
-    float z = a.part[i];
-    for (int j = 1; j < a.ks; ++j) z += a.part[(size_t)j * n + i];
-    ln_store(a, i, z + (a.bias ? a.bias[i % a.N] : 0.f));
   }
 }
 
@@ -250,26 +325,35 @@ bool make_matrix_map(CUtensorMap *map, const void *base, int rows, int cols, int
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN>
-cudaError_t launch(const uint16_t *x, int64_t ld, const uint16_t *w, int K, LnArgs a, cudaStream_t s) {
-  using C = LnCfg<BN>;
+template <int BN, bool SPLIT>
+cudaError_t launch(const uint16_t *x, int64_t ld, const uint16_t *w, int K, const LnArgs &a, cudaStream_t s) {
+  using C = LnCfg<BN, SPLIT>;
   CUtensorMap wmap, xmap;
   if (!make_matrix_map(&wmap, w, a.N, K, K, kLnM) || !make_matrix_map(&xmap, x, a.T, K, ld, BN))
     return cudaErrorInvalidValue;
-  const size_t smem = (size_t)C::kStages * C::kStageBytes + sizeof(LnBars<BN>) + 1024;
-  cudaError_t err = cudaFuncSetAttribute(linear_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const size_t smem = (size_t)C::kBarsAt + sizeof(LnBars<C::kStages>) + 1024;
+  cudaError_t err = cudaFuncSetAttribute(linear_kernel<BN, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  linear_kernel<BN><<<std::min(kLnWave, a.n_units), C::kThreads, smem, s>>>(wmap, xmap, a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(SPLIT ? a.n_units : std::min(kLnWave, a.n_units)));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  if (SPLIT) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)a.ks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, linear_kernel<BN, SPLIT>, wmap, xmap, a);
 }
 
 }  // namespace
 
-size_t linear_part_bytes() { return (size_t)kLnWave * kLnM * 64 * 4; }
-
 cudaError_t launch_linear(const uint16_t *x, int64_t ld, const uint16_t *w, const float *bias, int act,
-                          const float *resid, void *out, int T, int K, int N, float *part, uint32_t *status,
-                          cudaStream_t s) {
+                          const float *resid, void *out, int T, int K, int N, uint32_t *status, cudaStream_t s) {
   LnArgs a{};
   a.T = T;
   a.N = N;
@@ -279,22 +363,39 @@ cudaError_t launch_linear(const uint16_t *x, int64_t ld, const uint16_t *w, cons
   a.bias = bias;
   a.resid = resid;
   a.out = out;
-  a.part = part;
   a.status = status;
-  const int bn = T <= 16 ? 16 : (long long)a.n_ft * ((T + 127) / 128) < 74 ? 64 : 128;
-  const int tiles = a.n_ft * ((T + bn - 1) / bn);
-  a.ks = bn <= 64 ? std::max(1, std::min(kLnWave / tiles, (a.chunks + 3) / 4)) : 1;
-  a.n_units = tiles * a.ks;
+  // The tile that takes the fewest rounds of 64-wide chunks, each weighed by its products' cycles; where the tiles
+  // would leave more than half of the SMs idle, K split over a cluster.
+  auto tiles = [&](int bn) { return (long long)a.n_ft * ((T + bn - 1) / bn); };
+  int bn = 16;
+  if (T > 16) {
+    long long best = -1;
+    for (int c : {64, 128, 256}) {
+      if (c == 256 && resid) continue;
+      const long long t = tiles(c), cost = (t + kLnWave - 1) / kLnWave * (c == 64 ? 192 : c);
+      if (best < 0 || cost <= best) {
+        best = cost;
+        bn = c;
+      }
+    }
+    if (bn == 256 && tiles(256) < kLnWave) bn = 128;
+    if (bn == 128 && tiles(128) < kLnWave / 2) bn = 64;
+  }
+  a.ks = 1;
+  while (bn <= 128 && a.ks < 8 && tiles(bn) * a.ks * 2 <= (bn == 16 ? 2 : 1) * kLnWave && a.chunks / (a.ks * 2) >= 2) a.ks *= 2;
+  const long long units = tiles(bn) * a.ks;
+  if (units > 0x7fffffffll) return cudaErrorInvalidValue;
+  a.n_units = (int)units;
   a.slice = resid ? kLnSliceChunks : a.chunks;
   trace_mark(MOE_KERNEL_LINEAR, false, s);
-  cudaError_t err = bn == 16   ? launch<16>(x, ld, w, K, a, s)
-                    : bn == 64 ? launch<64>(x, ld, w, K, a, s)
-                               : launch<128>(x, ld, w, K, a, s);
-  if (err == cudaSuccess && a.ks > 1) {
-    const size_t n = (size_t)T * N;
-    linear_join_kernel<<<(unsigned)std::min<size_t>((n + 255) / 256, 1184), 256, 0, s>>>(a);
-    err = cudaGetLastError();
-  }
+  cudaError_t err;
+  if (a.ks > 1)
+    err = bn == 16 ? launch<16, true>(x, ld, w, K, a, s) : bn == 64 ? launch<64, true>(x, ld, w, K, a, s) : launch<128, true>(x, ld, w, K, a, s);
+  else
+    err = bn == 16    ? launch<16, false>(x, ld, w, K, a, s)
+          : bn == 64  ? launch<64, false>(x, ld, w, K, a, s)
+          : bn == 128 ? launch<128, false>(x, ld, w, K, a, s)
+                      : launch<256, false>(x, ld, w, K, a, s);
   trace_mark(MOE_KERNEL_LINEAR, true, s);
   return err;
 }
