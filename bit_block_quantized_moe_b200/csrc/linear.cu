@@ -7,6 +7,10 @@
 //                    past the end and columns past K read as zeros);
 //   MMA warp       : 4 tcgen05.mma per chunk, both operands in shared memory; two accumulators in tensor memory, so
 //                    that a tile's epilogue runs under the next tile's products;
+// Many tiles go to pairs of CTAs (tcgen05 cta_group::2): a pair's tile is 256 features x BN tokens, each CTA holds 128
+// weight rows, half of the token rows and the sums of its own features, and the first of them issues the products for
+// both.  What a SM has to fetch through L2 per product, which bounds the single-CTA form (85 bytes a nanosecond a SM),
+// falls by a third.
 //   epilogue warps : tensor memory lane quadrant = warp & 3; with 8 of them each has half of the columns.
 // With an fp32 output K runs in slices of 256: each slice has a fresh accumulator, added in fp32 to a running sum in
 // the epilogue's registers, because the tensor core's long accumulation truncates and loses up to 4e-6 of the result
@@ -123,6 +127,214 @@ __device__ __forceinline__ void ln_send(uint8_t *sums, int ks, int f, int t0, co
   const uint32_t at = cluster_map(smem_u32(sums), to) + (uint32_t)((cluster_rank() * BN + t0) * own + f - to * own) * 4u;
 #pragma unroll
   for (int n = 0; n < COUNT; ++n) cluster_store(at + (uint32_t)(n * own) * 4u, z[n]);
+}
+
+// ---- pairs of CTAs ----
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *holder_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(holder_smem)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// D[both CTAs' tensor memory] (+)= A[both CTAs' rows] * B[both CTAs' rows]^T, one K step of 16.
+__device__ __forceinline__ void umma_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on `bar` of both CTAs once the products issued so far are done.
+__device__ __forceinline__ void umma_commit_pair(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// A box to this CTA's memory, its bytes counted by the barrier at cluster address `bar` (the first CTA's).
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+template <int BN>
+struct LnPairCfg {
+  static constexpr int kThreads = 10 * 32;          // producer, products, 8 epilogue warps
+  static constexpr int kCols = BN / 2;              // columns an epilogue warp
+  static constexpr int kABytes = kLnM * kLnK * 2;
+  static constexpr int kBBytes = BN / 2 * kLnK * 2; // this CTA's half of the token rows
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = 196608 / kStageBytes;
+  static constexpr int kBarsAt = kStages * kStageBytes;
+};
+
+template <int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LnPairCfg<BN>::kThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, LnArgs a) {
+  using C = LnPairCfg<BN>;
+  extern __shared__ __align__(1024) uint8_t ln_raw[];
+  // the same place in both CTAs: descriptors and barriers of one serve the other
+  uint8_t *smem = ln_raw + ((1024u - (smem_u32(ln_raw) & 1023u)) & 1023u);
+  LnBars<C::kStages> &B = *reinterpret_cast<LnBars<C::kStages> *>(smem + C::kBarsAt);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank(), first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&B.full[i], 1);
+      mbar_init(&B.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B.dfull[i], 1);
+      mbar_init(&B.dempty[i], 16);  // both CTAs' epilogue warps (the first CTA's barrier)
+    }
+    mbar_init(&B.done, 1);
+    B.abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 0) tmem_alloc_pair(&B.tmem, 2 * BN);
+  tc_fence_before();
+  __syncthreads();
+  cluster_meet();  // both CTAs' barriers are ready
+  tc_fence_after();
+  const uint32_t tbase = B.tmem;
+
+  if (warp == 0) {
+    int cnt = 0, issued = 0;
+    bool live = true;
+    for (int u = first; u < a.n_units; u += step) {
+      const int ft = u % a.n_ft, tt = u / a.n_ft;
+      for (int c = 0; c < a.chunks; ++c, ++cnt) {
+        const int s = cnt % C::kStages;
+        if (live) live = __all_sync(0xffffffffu, ln_wait(&B.empty[s], ((cnt / C::kStages) & 1) ^ 1, B, a.status));
+        if (!live) continue;
+        issued = cnt + 1;
+        if (elect_one()) {
+          uint8_t *st = smem + s * C::kStageBytes;
+          const uint32_t bar = cluster_map(smem_u32(&B.full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&B.full[s], 2u * C::kStageBytes);
+          tma_load_2d_pair(st, &wmap, c * kLnK, ft * 256 + rank * kLnM, bar);
+          tma_load_2d_pair(st + C::kABytes, &xmap, c * kLnK, tt * BN + rank * (BN / 2), bar);
+        }
+        __syncwarp();
+      }
+    }
+    // Every copy issued must land before the CTAs exit: the first CTA's barriers count both CTAs' bytes.  (The second
+    // CTA's copies are waited for by the first, and neither leaves before the other: the meeting at the end.)
+    if (rank == 0)
+      for (int c2 = max(0, issued - C::kStages); c2 < issued; ++c2)
+        if (!mbar_wait(&B.full[c2 % C::kStages], (c2 / C::kStages) & 1)) set_status(a.status, kStatusTimeout);
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint32_t idesc = umma_idesc_bf16(256, BN);
+      int cnt = 0, sc = 0;
+      for (int u = first; u < a.n_units; u += step) {
+        for (int c = 0; c < a.chunks;) {
+          const int db = sc & 1;
+          ln_wait(&B.dempty[db], ((sc >> 1) & 1) ^ 1, B, a.status);
+          tc_fence_after();
+          const uint32_t dcol = tbase + db * BN;
+          const int e = min(a.chunks, c + a.slice);
+          for (int c0 = c; c < e; ++c, ++cnt) {
+            const int s = cnt % C::kStages;
+            ln_wait(&B.full[s], (cnt / C::kStages) & 1, B, a.status);
+            tc_fence_after();
+            const uint32_t st = smem_u32(smem + s * C::kStageBytes);
+            const uint64_t adesc = umma_sdesc_sw128(st), bdesc = umma_sdesc_sw128(st + C::kABytes);
+            if (elect_one()) {
+#pragma unroll
+              for (int j = 0; j < kLnK / 16; ++j)
+                umma_ss_pair(dcol, adesc + 2 * j, bdesc + 2 * j, idesc, (c != c0) | (j != 0));
+              umma_commit_pair(&B.empty[s]);
+            }
+            __syncwarp();
+          }
+          if (elect_one()) umma_commit_pair(&B.dfull[db]);
+          __syncwarp();
+          ++sc;
+        }
+      }
+      // all products have completed before tensor memory is released
+      if (elect_one()) {
+        umma_commit_pair(&B.done);
+        if (!mbar_wait(&B.done, 0)) set_status(a.status, kStatusTimeout);
+      }
+      __syncwarp();
+    }
+  } else {
+    const int q = warp & 3, part = (warp - 2) >> 2;
+    const uint32_t tcol = tbase + ((uint32_t)(32 * q) << 16) + part * C::kCols;
+    const uint32_t dempty0 = cluster_map(smem_u32(&B.dempty[0]), 0), dempty1 = cluster_map(smem_u32(&B.dempty[1]), 0);
+    int sc = 0;
+    for (int u = first; u < a.n_units; u += step) {
+      const int ft = u % a.n_ft, tt = u / a.n_ft;
+      const int f = ft * 256 + rank * kLnM + 32 * q + lane, t0 = tt * BN + part * C::kCols;
+      const float b = a.bias && f < a.N ? a.bias[f] : 0.f;
+      if (BN == 256 || a.slice >= a.chunks) {
+        ln_wait(&B.dfull[sc & 1], (sc >> 1) & 1, B, a.status);
+        tc_fence_after();
+#pragma unroll 1
+        for (int h = 0; h < C::kCols; h += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tcol + (sc & 1) * BN + h, v);
+          tmem_wait_ld();
+          float z[32];
+#pragma unroll
+          for (int n = 0; n < 32; ++n) z[n] = __uint_as_float(v[n]) + b;
+          if (f < a.N) ln_finish(a, (size_t)(t0 + h) * a.N + f, (size_t)a.N, z, a.T - t0 - h);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(sc & 1 ? dempty1 : dempty0);
+        ++sc;
+      } else if constexpr (BN == 128) {
+        float run[C::kCols];
+#pragma unroll
+        for (int n = 0; n < C::kCols; ++n) run[n] = b;
+        for (int c = 0; c < a.chunks; c += a.slice, ++sc) {
+          ln_wait(&B.dfull[sc & 1], (sc >> 1) & 1, B, a.status);
+          tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < C::kCols; h += 32) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(tcol + (sc & 1) * BN + h, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int n = 0; n < 32; ++n) run[h + n] += __uint_as_float(v[n]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(sc & 1 ? dempty1 : dempty0);
+        }
+#pragma unroll
+        for (int h = 0; h < C::kCols; h += 32) {
+          float z[32];
+#pragma unroll
+          for (int n = 0; n < 32; ++n) z[n] = run[h + n];
+          if (f < a.N) ln_finish(a, (size_t)(t0 + h) * a.N + f, (size_t)a.N, z, a.T - t0 - h);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (rank == 1 && warp == 1) mbar_wait(&B.done, 0);  // this CTA's copy of the last arrival (the first CTA reports)
+  __syncwarp();
+  cluster_meet();  // neither CTA leaves, or frees tensor memory, while the other's products or copies need it
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc_pair(tbase, 2 * BN);
+  }
 }
 
 template <int BN, bool SPLIT>
@@ -350,6 +562,19 @@ cudaError_t launch(const uint16_t *x, int64_t ld, const uint16_t *w, int K, cons
   return cudaLaunchKernelEx(&cfg, linear_kernel<BN, SPLIT>, wmap, xmap, a);
 }
 
+template <int BN>
+cudaError_t launch_pair(const uint16_t *x, int64_t ld, const uint16_t *w, int K, LnArgs a, cudaStream_t s) {
+  using C = LnPairCfg<BN>;
+  CUtensorMap wmap, xmap;
+  if (!make_matrix_map(&wmap, w, a.N, K, K, kLnM) || !make_matrix_map(&xmap, x, a.T, K, ld, BN / 2))
+    return cudaErrorInvalidValue;
+  const size_t smem = (size_t)C::kBarsAt + sizeof(LnBars<C::kStages>) + 1024;
+  cudaError_t err = cudaFuncSetAttribute(linear_pair_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  linear_pair_kernel<BN><<<2 * std::min(kLnWave / 2, a.n_units), C::kThreads, smem, s>>>(wmap, xmap, a);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_linear(const uint16_t *x, int64_t ld, const uint16_t *w, const float *bias, int act,
@@ -382,11 +607,24 @@ cudaError_t launch_linear(const uint16_t *x, int64_t ld, const uint16_t *w, cons
     if (bn == 128 && tiles(128) < kLnWave / 2) bn = 64;
   }
   a.ks = 1;
+  a.slice = resid ? kLnSliceChunks : a.chunks;
+  // pairs of CTAs, once their tiles fill most of the SMs
+  const int n_ft2 = (N + 255) / 256, pair = resid ? 128 : 256;
+  for (int c = pair; c >= 128; c /= 2) {
+    const long long t = (long long)n_ft2 * ((T + c - 1) / c);
+    if (t * 4 < kLnWave / 2 * 3) continue;
+    if (t > 0x7fffffffll) return cudaErrorInvalidValue;
+    a.n_ft = n_ft2;
+    a.n_units = (int)t;
+    trace_mark(MOE_KERNEL_LINEAR, false, s);
+    const cudaError_t err = c == 256 ? launch_pair<256>(x, ld, w, K, a, s) : launch_pair<128>(x, ld, w, K, a, s);
+    trace_mark(MOE_KERNEL_LINEAR, true, s);
+    return err;
+  }
   while (bn <= 128 && a.ks < 8 && tiles(bn) * a.ks * 2 <= (bn == 16 ? 2 : 1) * kLnWave && a.chunks / (a.ks * 2) >= 2) a.ks *= 2;
   const long long units = tiles(bn) * a.ks;
   if (units > 0x7fffffffll) return cudaErrorInvalidValue;
   a.n_units = (int)units;
-  a.slice = resid ? kLnSliceChunks : a.chunks;
   trace_mark(MOE_KERNEL_LINEAR, false, s);
   cudaError_t err;
   if (a.ks > 1)
