@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int groups = a.V * w.row_tiles, rows = a.kv.per * a.G;
   const uint32_t smem0 = smem_u32(win_smem);
+  pdl_release();
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&B.full[i], 33);  // the producer's expected bytes, and its lanes' copies of queries
@@ -185,6 +186,8 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
   }
 
   for (int i = threadIdx.x; i < w.row_tiles * C::kRows; i += C::kThreads) tok_s[i] = (uint8_t)min(i / a.G, 255);
+
+  pdl_wait();
 
   // ---- the length of the line, and its shares
   if (blockIdx.x == 0) check_sequences(a.kv, a.T, a.status);
@@ -706,8 +709,7 @@ cudaError_t launch(WinArgs w, const moe_kv_cache &c, cudaStream_t s) {
   w.row_tiles = (w.a.kv.per * w.a.G + C::kRows - 1) / C::kRows;
   cudaError_t err = cudaFuncSetAttribute(attn_window_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (err != cudaSuccess) return err;
-  attn_window_kernel<D, NR><<<kAttnSms * C::kCtas, C::kThreads, C::kSmem, s>>>(km, vm, w);
-  return cudaGetLastError();
+  return launch_dependent(attn_window_kernel<D, NR>, kAttnSms * C::kCtas, C::kThreads, C::kSmem, 1, s, km, vm, w);
 }
 
 // Rows of a window: one, two, four or eight 8-row tiles side by side; more rows than 64 walk the keys again.

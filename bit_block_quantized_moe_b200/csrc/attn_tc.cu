@@ -104,6 +104,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const AttnArgs &a = w.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hv = blockIdx.x % a.V, item = blockIdx.x / a.V;
+  pdl_release();
+  pdl_wait();
 
   // ---- which rows: items count row-tile pairs from the last sequence's last pair (with a causal mask the largest)
   if (blockIdx.x == 0) check_sequences(a.kv, a.T, a.status);
@@ -481,8 +483,7 @@ cudaError_t launch_tc(const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) 
   const size_t smem = (size_t)C::kSmemTiles * C::kTileBytes + sizeof(TcBars<D>) + 1024;
   cudaError_t err = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  attn_tc_kernel<D><<<(unsigned)(items * a.V), kTcThreads, smem, s>>>(qm, km, vm, w);
-  return cudaGetLastError();
+  return launch_dependent(attn_tc_kernel<D>, (unsigned)(items * a.V), kTcThreads, smem, 1, s, qm, km, vm, w);
 }
 
 }  // namespace

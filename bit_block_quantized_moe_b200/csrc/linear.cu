@@ -12,9 +12,10 @@
 // both.  What a SM has to fetch through L2 per product, which bounds the single-CTA form (85 bytes a nanosecond a SM),
 // falls by a third.
 //   epilogue warps : tensor memory lane quadrant = warp & 3; with 8 of them each has half of the columns.
-// With an fp32 output K runs in slices of 256: each slice has a fresh accumulator, added in fp32 to a running sum in
-// the epilogue's registers, because the tensor core's long accumulation truncates and loses up to 4e-6 of the result
-// at K = 2048, which bf16 hides and fp32 does not.  When the tiles alone leave SMs idle, a cluster of 2, 4 or 8 CTAs
+// With an fp32 output K runs in slices of 512: each slice has a fresh accumulator, added in fp32 to a running sum in
+// the epilogue's registers, because the tensor core's long accumulation truncates: without a residual K = 2048 is
+// 2.1e-6 of the result off and K = 4096 4.4e-6, which bf16 hides and fp32 does not; in slices of 512 it is 4.7e-7 at
+// any K (an fp32 product in software: 3.9e-7 and 6.1e-7), in slices of 256 2.4e-7 but 14% slower.  When the tiles alone leave SMs idle, a cluster of 2, 4 or 8 CTAs
 // splits K: each sends the others their features' parts through distributed shared memory and finishes its own,
 // summed in rank order.  Every wait is bounded (sync.cuh).
 #include <algorithm>
@@ -27,13 +28,13 @@ namespace {
 
 constexpr int kLnM = 128;         // features a tile
 constexpr int kLnK = 64;          // K a chunk: one 128-byte swizzle row
-constexpr int kLnSliceChunks = 4;  // chunks a slice, fp32 output
+constexpr int kLnSliceChunks = 8;  // chunks a slice, fp32 output
 constexpr int kLnWave = 148;
 
 // SPLIT: clusters share K, a tile a CTA.  Otherwise persistent CTAs.
 template <int BN, bool SPLIT>
 struct LnCfg {
-  static constexpr int kEpiWarps = BN >= 128 ? 8 : 4;
+  static constexpr int kEpiWarps = BN >= 64 ? 8 : 4;
   static constexpr int kThreads = (2 + kEpiWarps) * 32;
   static constexpr int kCols = BN * 4 / kEpiWarps;  // columns an epilogue warp
   static constexpr int kABytes = kLnM * kLnK * 2;
@@ -82,7 +83,7 @@ template <int COUNT>
 __device__ __forceinline__ void ln_finish(const LnArgs &a, size_t i0, size_t step, float (&z)[COUNT], int ok) {
   if (a.act == MOE_ACT_SILU) {
 #pragma unroll
-    for (int n = 0; n < COUNT; ++n) z[n] = z[n] / (1.0f + __expf(-z[n]));
+    for (int n = 0; n < COUNT; ++n) z[n] = __fdividef(z[n], 1.0f + __expf(-z[n]));
   } else if (a.act == MOE_ACT_GELU) {
 #pragma unroll
     for (int n = 0; n < COUNT; ++n) z[n] = 0.5f * z[n] * (1.0f + erff(z[n] * 0.70710678118654752f));
@@ -179,7 +180,7 @@ struct LnPairCfg {
 };
 
 template <int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LnPairCfg<BN>::kThreads, 1)
+__global__ void __launch_bounds__(LnPairCfg<BN>::kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, LnArgs a) {
   using C = LnPairCfg<BN>;
   extern __shared__ __align__(1024) uint8_t ln_raw[];
@@ -187,6 +188,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LnPairCfg<BN>::kThre
   uint8_t *smem = ln_raw + ((1024u - (smem_u32(ln_raw) & 1023u)) & 1023u);
   LnBars<C::kStages> &B = *reinterpret_cast<LnBars<C::kStages> *>(smem + C::kBarsAt);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_release();
   const int rank = (int)cluster_rank(), first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
@@ -207,6 +209,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LnPairCfg<BN>::kThre
   __syncthreads();
   cluster_meet();  // both CTAs' barriers are ready
   tc_fence_after();
+  pdl_wait();
   const uint32_t tbase = B.tmem;
 
   if (warp == 0) {
@@ -345,6 +348,7 @@ __global__ void __launch_bounds__(LnCfg<BN, SPLIT>::kThreads, 1)
   uint8_t *smem = ln_raw + ((1024u - (smem_u32(ln_raw) & 1023u)) & 1023u);
   LnBars<C::kStages> &B = *reinterpret_cast<LnBars<C::kStages> *>(smem + C::kBarsAt);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_release();
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -364,6 +368,7 @@ __global__ void __launch_bounds__(LnCfg<BN, SPLIT>::kThreads, 1)
   if constexpr (SPLIT) cluster_meet();  // every CTA of the cluster is there before its memory is written
   __syncthreads();
   tc_fence_after();
+  pdl_wait();
   const uint32_t tbase = B.tmem;
 
   if (warp == 0) {
@@ -546,20 +551,8 @@ cudaError_t launch(const uint16_t *x, int64_t ld, const uint16_t *w, int K, cons
   const size_t smem = (size_t)C::kBarsAt + sizeof(LnBars<C::kStages>) + 1024;
   cudaError_t err = cudaFuncSetAttribute(linear_kernel<BN, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(SPLIT ? a.n_units : std::min(kLnWave, a.n_units)));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  if (SPLIT) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)a.ks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  }
-  return cudaLaunchKernelEx(&cfg, linear_kernel<BN, SPLIT>, wmap, xmap, a);
+  return launch_dependent(linear_kernel<BN, SPLIT>, (unsigned)(SPLIT ? a.n_units : std::min(kLnWave, a.n_units)),
+                          C::kThreads, smem, (unsigned)a.ks, s, wmap, xmap, a);
 }
 
 template <int BN>
@@ -571,8 +564,8 @@ cudaError_t launch_pair(const uint16_t *x, int64_t ld, const uint16_t *w, int K,
   const size_t smem = (size_t)C::kBarsAt + sizeof(LnBars<C::kStages>) + 1024;
   cudaError_t err = cudaFuncSetAttribute(linear_pair_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  linear_pair_kernel<BN><<<2 * std::min(kLnWave / 2, a.n_units), C::kThreads, smem, s>>>(wmap, xmap, a);
-  return cudaGetLastError();
+  return launch_dependent(linear_pair_kernel<BN>, 2u * std::min(kLnWave / 2, a.n_units), C::kThreads, smem, 2, s, wmap,
+                          xmap, a);
 }
 
 }  // namespace

@@ -16,6 +16,7 @@
 #include <algorithm>
 
 #include "attn.cuh"
+#include "sync.cuh"
 
 namespace moe {
 namespace {
@@ -62,6 +63,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) qk_norm_rope_kernel(const __g
   __shared__ float2 cs[2][kTok][64];
   __shared__ int pos_s[2][kTok];
   __shared__ int64_t row_s[2][kTok];
+  pdl_release();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = threadIdx.x / kGroup, sub = threadIdx.x % kGroup;
   const int tt = group / kStep, h0 = group % kStep;
@@ -113,6 +115,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) qk_norm_rope_kernel(const __g
       cs[par][warp][lane + 32 * e] = make_float2(cn, sn);
     }
   };
+  pdl_wait();
   float gq[16], gk[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
@@ -216,12 +219,10 @@ cudaError_t launch_qk_norm_rope(const moe_attn_dims &d, const uint16_t *qkv, int
   const moe_rope &r = rope ? *rope : none;
   const unsigned grid = (unsigned)std::min((T + kTok - 1) / kTok, 2 * 148);  // two CTAs a SM
   trace_mark(MOE_KERNEL_QK_NORM, false, s);
-  if (d.head_dim == 128)
-    qk_norm_rope_kernel<128><<<grid, kNormThreads, 0, s>>>(a, r);
-  else
-    qk_norm_rope_kernel<64><<<grid, kNormThreads, 0, s>>>(a, r);
+  const cudaError_t err = d.head_dim == 128 ? launch_dependent(qk_norm_rope_kernel<128>, grid, kNormThreads, 0, 1, s, a, r)
+                                            : launch_dependent(qk_norm_rope_kernel<64>, grid, kNormThreads, 0, 1, s, a, r);
   trace_mark(MOE_KERNEL_QK_NORM, true, s);
-  return cudaGetLastError();
+  return err;
 }
 
 }  // namespace moe

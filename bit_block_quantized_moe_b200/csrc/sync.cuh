@@ -84,6 +84,13 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void *src, uint32_t bytes
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
+// ---- programmatic dependent launch ------------------------------------------------
+// pdl_release: the next launch of the stream may set itself up on SMs that this grid leaves.  pdl_wait: every earlier
+// launch has completed and its writes are visible; nothing that another launch writes, or reads from what this one
+// writes, is touched before.
+__device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---- CTA-level ---------------------------------------------------------------------
 __device__ __forceinline__ void named_bar(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
@@ -144,6 +151,27 @@ __device__ __forceinline__ bool grid_wait(const uint64_t *count, uint64_t target
   }
   named_bar(bar_id, nthreads);
   return *(volatile int *)flag_smem == 0;
+}
+
+// Launches `kernel` as a programmatic dependent of what precedes it on the stream (it calls pdl_wait), in clusters of
+// `cluster` CTAs.
+template <class... P, class... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, unsigned cluster,
+                                    cudaStream_t s, const A &...args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace moe
