@@ -737,9 +737,11 @@ bool make_pages_map(CUtensorMap *map, const uint16_t *cache, int n_pages, const 
 }
 
 size_t attn_part_bytes(const moe_attn_dims &d, int, int) {
+  // of windows two parts a share (with more than 32 rows, one CTA a SM, there are half as many shares); of chunks one a
+  // CTA of a cluster, with at most kAttnSms CTAs where there are clusters
   const int rows = 8 * d.n_heads / d.n_kv_heads;  // the most rows of a window, then those of a CTA
-  // two parts a share; with more than 32 rows (one CTA a SM) there are half as many shares
-  return (size_t)kAttnShares * 2 * (rows <= 8 ? 8 : rows <= 16 ? 16 : 32) * (d.head_dim + 2) * 4;
+  const size_t windows = (size_t)kAttnShares * 2 * (rows <= 8 ? 8 : rows <= 16 ? 16 : 32) * (d.head_dim + 2) * 4;
+  return std::max(windows, (size_t)kAttnSms * 256 * d.head_dim * 4);
 }
 
 cudaError_t launch_attn(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) {

@@ -14,7 +14,9 @@
 //   warp 9         : tcgen05.mma issue;
 //   warps 10, 11   : V rows that must not be multiplied (keys that no row sees, non-finite values behind a mask)
 //                    are cleared before P V, in tiles with a mask only.
-// Every wait is bounded (sync.cuh).
+// Few row tiles over many keys leave SMs idle: then a cluster of 2, 4 or 8 CTAs shares the key tiles of one pair of row
+// tiles.  Each finishes its part of the rows from all of their (m, l, O), in rank order.
+// Every wait on memory is bounded (sync.cuh).
 #include <algorithm>
 
 #include "attn.cuh"
@@ -49,17 +51,20 @@ struct TileInfo {
 template <int D>
 struct TcBars {
   uint64_t q_full, k_full[TcCfg<D>::kStages], k_empty[TcCfg<D>::kStages], v_full[TcCfg<D>::kStages],
-      v_ready[TcCfg<D>::kStages], v_empty[TcCfg<D>::kStages], s_full[2], p_ready[2], pv_done[2], done;
+      v_ready[TcCfg<D>::kStages], v_empty[TcCfg<D>::kStages], s_full[2], p_ready[2][2], pv_done[2], done;
   TileInfo info[kTcInfo];
   uint32_t flagged[TcCfg<D>::kStages][4];  // keys of a V stage whose values are not finite
   uint32_t tmem;
   int abort;
+  uint8_t tok[128];  // token of each row of a tile, w.tokens for the rows behind the last
+  float2 ml[256];  // maximum and sum of each row, for the other CTAs of a cluster
   int found_b, found_t, warp_sum[kTcThreads / 32];
 };
 
 struct TcArgs {
   AttnArgs a;
   int tokens;  // tokens a row tile: 128 / G
+  int log_splits;  // log2 of the CTAs of a cluster, which share an item's key tiles
 };
 
 template <class Bars>
@@ -80,9 +85,9 @@ __device__ __forceinline__ uint64_t sdesc_n_sw128(uint32_t addr, uint32_t group_
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) {
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 
@@ -90,6 +95,53 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   float y;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
+}
+
+// Where the rows of a pair of row tiles go.
+struct TcRows {
+  uint16_t *out;  // of the sequence's first new token and the group's first head
+  int H, G, tok0, tokens, m, nq;
+};
+
+// The rows of one CTA of a cluster of 2^LS: row k * 2^LS + split for k = first, first + step, ..., all parts of all rows
+// of a lane in flight at once.  `mine`: this CTA's part in shared memory; `parts`: the others'.
+template <int D, int LS>
+__device__ __forceinline__ void tc_join(const TcRows &w, const float2 *ml, const uint8_t *tok, const float *mine,
+                                        const float *parts, int split, int first, int sub) {
+  constexpr int kQuads = D / 4, kStep = 8 * (32 / kQuads), kOwn = 256 >> LS, kRows = kOwn / kStep, kParts = 1 << LS;
+  float4 o[kRows][kParts];
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const int r = ((first + u * kStep) << LS) + split, q = min(r, w.nq * 128 - kParts + split);  // rows that are there
+#pragma unroll
+    for (int p = 0; p < kParts; ++p)
+      o[u][p] = p == split ? *reinterpret_cast<const float4 *>(mine + (size_t)q * D + ((sub ^ (q & (kQuads - 1))) << 2))
+                           : __ldcg(reinterpret_cast<const float4 *>(parts + ((size_t)p * 256 + q) * D) + sub);
+  }
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const int k = first + u * kStep, r = (k << LS) + split, i = r >> 7, rt = tok[r & 127];
+    const int tk = w.tok0 + i * w.tokens + rt;
+    if (i >= w.nq || rt >= w.tokens || tk >= w.m) continue;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) mx = fmaxf(mx, ml[p * kOwn + k].x);
+    const float sub_m = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      const float2 x = ml[p * kOwn + k];
+      const float f = ex2(x.x - sub_m);
+      sum += f * x.y;
+      y[0] += f * o[u][p].x;
+      y[1] += f * o[u][p].y;
+      y[2] += f * o[u][p].z;
+      y[3] += f * o[u][p].w;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    uint16_t *dst = w.out + ((size_t)tk * w.H + (r & 127) - rt * w.G) * D + sub * 4;
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv));
+  }
 }
 
 template <int D>
@@ -103,7 +155,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   TcBars<D> &B = *reinterpret_cast<TcBars<D> *>(smem + C::kSmemTiles * C::kTileBytes);
   const AttnArgs &a = w.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hv = blockIdx.x % a.V, item = blockIdx.x / a.V;
+  const int splits = 1 << w.log_splits, split = blockIdx.x & (splits - 1), unit = blockIdx.x >> w.log_splits, hv = unit % a.V, item = unit / a.V;
   pdl_release();
   pdl_wait();
 
@@ -145,9 +197,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int base = s.n - s.m;
   const int p0 = base + tok0, p1 = base + min(s.m, tok0 + pair) - 1;
   const TileRange tr = tile_range(p0, p1, s.n, a.window, a.n_sinks, kTcLogBK);
-  const int nt = tr.count;
+  // this CTA's key tiles: t0 .. t0 + nt - 1 of the range
+  const int tile0 = (int)((long long)tr.count * split >> w.log_splits);
+  const int nt = (int)((long long)tr.count * (split + 1) >> w.log_splits) - tile0;
   const int32_t *table = a.kv.table + (size_t)b * a.kv.max_pages;
 
+  if (threadIdx.x < 128) B.tok[threadIdx.x] = (uint8_t)min((int)threadIdx.x / a.G, w.tokens);
   if (threadIdx.x == 0) {
     mbar_init(&B.q_full, 1);
     for (int i = 0; i < C::kStages; ++i) {
@@ -159,7 +214,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.s_full[i], 1);
-      mbar_init(&B.p_ready[i], 4);
+      mbar_init(&B.p_ready[i][0], 4);
+      mbar_init(&B.p_ready[i][1], 4);
       mbar_init(&B.pv_done[i], 1);
     }
     mbar_init(&B.done, 1);
@@ -171,7 +227,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = B.tmem;
+  float m = -INFINITY, l = 0.f;  // of a row, in its softmax thread: m in units of log2, scaled
 
+  // Registers go from the last four warps to the softmax: 256 x 216 + 128 x 72 are the launch's 384 x 168.
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 8) {
     // ---- producer ----
     const int rows = w.tokens * a.G;
@@ -186,7 +246,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int ps = 1 << a.kv.log_ps, pages = kTcBK >> a.kv.log_ps;
     int issued_k = 0, issued_v = 0;
     for (int t = 0; t < nt; ++t) {
-      const int st = t % C::kStages, j0 = tile_of(tr, t) << kTcLogBK;
+      const int st = t % C::kStages, j0 = tile_of(tr, tile0 + t) << kTcLogBK;
       const uint32_t ph = ((t / C::kStages) & 1) ^ 1;
       if (!__all_sync(0xffffffffu, at_wait(&B.k_empty[st], ph, B, a.status))) break;
       // lane l < pages: page l of the tile
@@ -256,22 +316,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int st = t % C::kStages;
       const uint32_t ph = (t / C::kStages) & 1;
       for (int i = 0; i < nq; ++i) {
-        at_wait(&B.p_ready[i], t & 1, B, a.status);
-        if (i == 0) {
-          at_wait(&B.v_full[st], ph, B, a.status);
-          at_wait(&B.v_ready[st], ph, B, a.status);
-        }
-        tc_fence_after();
         const uint32_t va = smem_u32(v_s) + st * C::kTileBytes;
-        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kTcBK / 16; ++k)
-            umma_ts(tbase + C::kO + i * D, tbase + C::kS + i * kTcBK + k * 8, sdesc_n_sw128(va + k * 2048, C::kHalfBytes),
-                    idesc_o, (t | k) != 0);
-          umma_commit(&B.pv_done[i]);
-          if (i == nq - 1) umma_commit(&B.v_empty[st]);
+        for (int h = 0; h < 2; ++h) {  // the weights of the first 64 keys, then the others'
+          at_wait(&B.p_ready[i][h], t & 1, B, a.status);
+          if (i == 0 && h == 0) {
+            at_wait(&B.v_full[st], ph, B, a.status);
+            at_wait(&B.v_ready[st], ph, B, a.status);
+          }
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 4 * h; k < 4 * h + 4; ++k)
+              umma_ts(tbase + C::kO + i * D, tbase + C::kS + i * kTcBK + k * 8, sdesc_n_sw128(va + k * 2048, C::kHalfBytes),
+                      idesc_o, (t | k) != 0);
+            if (h == 1) {
+              umma_commit(&B.pv_done[i]);
+              if (i == nq - 1) umma_commit(&B.v_empty[st]);
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
         if (t + 1 < nt) {
           if (i == 0) at_wait(&B.k_full[(t + 1) % C::kStages], ((t + 1) / C::kStages) & 1, B, a.status);
           at_wait(&B.pv_done[i], t & 1, B, a.status);  // S_i(t + 1) goes over P_i(t)
@@ -285,10 +350,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!mbar_wait(&B.done, 0)) set_status(a.status, kStatusTimeout);
     }
     __syncwarp();
-  } else if (warp >= 10) {
+  } else {
     // ---- V rows that must not be multiplied ----
     for (int t = 0; t < nt; ++t) {
-      const int st = t % C::kStages, j0 = tile_of(tr, t) << kTcLogBK;
+      const int st = t % C::kStages, j0 = tile_of(tr, tile0 + t) << kTcLogBK;
       at_wait(&B.v_full[st], (t / C::kStages) & 1, B, a.status);
       const TileInfo &in = B.info[t % kTcInfo];
       if (in.partial) {
@@ -320,7 +385,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_arrive(&B.v_empty[st]);
       }
     }
+  }
+  if (splits > 1) {  // the meetings of the cluster's parts, below
+    __syncthreads();
+    cluster_meet();
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---- softmax of row tile i: one thread a row ----
     const int i = warp >> 2, row = threadIdx.x & 127;
     if (i < nq) {
@@ -330,9 +401,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
       const uint32_t ts = tbase + lanes + C::kS + i * kTcBK, to = tbase + lanes + C::kO + i * D;
       const float scale = a.scale_log2;
-      float m = -INFINITY, l = 0.f;  // m in units of log2, scaled
       for (int t = 0; t < nt; ++t) {
-        const int st = t % C::kStages, j0 = tile_of(tr, t) << kTcLogBK;
+        const int st = t % C::kStages, j0 = tile_of(tr, tile0 + t) << kTcLogBK;
         at_wait(&B.s_full[i], t & 1, B, a.status);
         tc_fence_after();
         const TileInfo &in = B.info[t % kTcInfo];
@@ -358,13 +428,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (scale >= 0.f) {
           float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
 #pragma unroll
-          for (int c = 4; c < 128; c += 4) {
-            m0 = max_nan(m0, x[c]);
-            m1 = max_nan(m1, x[c + 1]);
-            m2 = max_nan(m2, x[c + 2]);
-            m3 = max_nan(m3, x[c + 3]);
+          for (int c = 4; c + 7 < 128; c += 8) {
+            m0 = max3_nan(m0, x[c], x[c + 1]);
+            m1 = max3_nan(m1, x[c + 2], x[c + 3]);
+            m2 = max3_nan(m2, x[c + 4], x[c + 5]);
+            m3 = max3_nan(m3, x[c + 6], x[c + 7]);
           }
-          mx = max_nan(max_nan(m0, m1), max_nan(m2, m3));
+          m0 = max3_nan(m0, x[124], x[125]);
+          m1 = max3_nan(m1, x[126], x[127]);
+          mx = max3_nan(max3_nan(m0, m1, m2), m3, m3);
         } else {
           mx = x[0];
 #pragma unroll
@@ -398,20 +470,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         const float sub = m == -INFINITY ? 0.f : m;
-        float l0 = 0.f, l1 = 0.f;
+        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t p[32];
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float y0 = ex2(fmaf(x[c + e], scale, -sub)), y1 = ex2(fmaf(x[c + e + 1], scale, -sub));
-            l0 += y0;
-            l1 += y1;
-            p[e / 2] = pack_bf16x2(y0, y1);
+          for (int c = 64 * h; c < 64 * h + 64; c += 32) {
+            uint32_t p[32];
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              float y0 = -sub, y1 = -sub, y2 = -sub, y3 = -sub;
+              fma2(y0, y1, x[c + e], x[c + e + 1], scale, scale);
+              fma2(y2, y3, x[c + e + 2], x[c + e + 3], scale, scale);
+              y0 = ex2(y0);
+              y1 = ex2(y1);
+              y2 = ex2(y2);
+              y3 = ex2(y3);
+              add2(l0, l1, y0, y1);
+              add2(l2, l3, y2, y3);
+              p[e / 2] = pack_bf16x2(y0, y1);
+              p[e / 2 + 1] = pack_bf16x2(y2, y3);
+            }
+            tmem_st_32x32b_x16(ts + c / 2, p);
           }
-          tmem_st_32x32b_x16(ts + c / 2, p);
+          if (h == 0) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.p_ready[i][0]);
+          }
         }
-        l += l0 + l1;
+        l += (l0 + l1) + (l2 + l3);
         if (in.partial) {
           // a value that is not finite was left out of P V: rows that see it become NaN
           at_wait(&B.v_ready[st], (t / C::kStages) & 1, B, a.status);
@@ -422,31 +510,96 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B.p_ready[i]);
+        if (lane == 0) mbar_arrive(&B.p_ready[i][1]);
       }
-      // ---- output rows ----
-      if (nt > 0) at_wait(&B.pv_done[i], (nt - 1) & 1, B, a.status);
-      tc_fence_after();
-      const float inv = l == 0.f ? 0.f : 1.0f / l;
-      uint16_t *dst = a.out + ((size_t)(s.q0 + tok) * a.H + (size_t)hv * a.G + row % a.G) * D;
+      if (splits == 1) {
+        // ---- output rows ----
+        if (nt > 0) at_wait(&B.pv_done[i], (nt - 1) & 1, B, a.status);
+        tc_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        // through the query tile's place (its products are done), so that a warp writes whole rows
+        uint8_t *os = q_s + i * C::kTileBytes + row * (D * 2);
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t v[32];
-        if (nt > 0) {
-          tmem_ld_32x32b_x32(to + c, v);
-          tmem_wait_ld();
-        }
-        if (alive) {
+        for (int c = 0; c < D; c += 32) {
+          uint32_t v[32];
+          if (nt > 0) {
+            tmem_ld_32x32b_x32(to + c, v);
+            tmem_wait_ld();
+          }
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             uint32_t o[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               o[k] = nt > 0 && l != 0.f ? pack_bf16x2(__uint_as_float(v[e + 2 * k]) * inv, __uint_as_float(v[e + 2 * k + 1]) * inv) : 0u;
-            *reinterpret_cast<uint4 *>(dst + c + e) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(os + ((((c + e) >> 3) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
+        __syncwarp();
+        constexpr int kPieces = D / 8, kRowsOnce = 32 / kPieces;
+        const int wrow = 32 * (warp & 3);
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += kRowsOnce) {
+          const int r = wrow + r0 + lane / kPieces, ch = lane % kPieces;
+          const int rt = B.tok[r], tk = tok0 + i * w.tokens + rt;
+          if (rt >= w.tokens || tk >= s.m) continue;
+          const uint4 o = *reinterpret_cast<const uint4 *>(q_s + i * C::kTileBytes + r * (D * 2) + ((ch ^ (r & 7)) << 4));
+          *reinterpret_cast<uint4 *>(a.out + ((size_t)(s.q0 + tk) * a.H + (size_t)hv * a.G + r - rt * a.G) * D + ch * 8) = o;
+        }
       }
+    }
+    if (splits > 1) {
+      // ---- the cluster's parts: O of this CTA's keys into the stages' place, rows of D fp32 in swizzled 16-byte
+      // pieces.  CTA r mod splits finishes row r: it gets the others' (m, l) into its shared memory, and their rows by
+      // way of the workspace (L2 carries whole rows at once; fetched through distributed shared memory 64 KB took
+      // 7.5 us).
+      constexpr int kQuads = D / 4;
+      const int own = 256 >> w.log_splits;
+      __syncthreads();  // no product or copy needs the stages any more
+      if ((warp >> 2) < nq) {
+        const int i = warp >> 2, row = threadIdx.x & 127, r = i * 128 + row;
+        const uint32_t to = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + C::kO + i * D;
+        float *os = reinterpret_cast<float *>(k_s) + (size_t)r * D;
+        if (nt > 0) {
+          at_wait(&B.pv_done[i], (nt - 1) & 1, B, a.status);
+          tc_fence_after();
+        }
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t v[32];
+          if (nt > 0) {
+            tmem_ld_32x32b_x32(to + c, v);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = 0;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4 *>(os + ((((c + e) >> 2) ^ (row & (kQuads - 1))) << 2)) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+        const int k = r >> w.log_splits, owner = r & (splits - 1);
+        cluster_store2(cluster_map(smem_u32(&B.ml[split * own + k]), owner), m, l);
+      }
+      named_bar(1, 256);
+      constexpr int kRowsOnce = 32 / kQuads;
+      const int sub = lane % kQuads, first = warp * kRowsOnce + lane / kQuads;
+      float *parts = a.part + (size_t)(blockIdx.x - split) * 256 * D;  // of the cluster
+      const float *mine = reinterpret_cast<const float *>(k_s);
+#pragma unroll 8
+      for (int r = first; r < nq * 128; r += 8 * kRowsOnce)
+        if ((r & (splits - 1)) != split)
+          __stcg(reinterpret_cast<float4 *>(parts + ((size_t)split * 256 + r) * D) + sub,
+                 *reinterpret_cast<const float4 *>(mine + (size_t)r * D + ((sub ^ (r & (kQuads - 1))) << 2)));
+      __syncwarp();
+      cluster_meet();  // releases and acquires what went to the workspace too
+      const TcRows where{a.out + ((size_t)s.q0 * a.H + (size_t)hv * a.G) * D, a.H, a.G, tok0, w.tokens, s.m, nq};
+      if (w.log_splits == 1)
+        tc_join<D, 1>(where, B.ml, B.tok, mine, parts, split, first, sub);
+      else if (w.log_splits == 2)
+        tc_join<D, 2>(where, B.ml, B.tok, mine, parts, split, first, sub);
+      else
+        tc_join<D, 3>(where, B.ml, B.tok, mine, parts, split, first, sub);
     }
   }
   tc_fence_before();
@@ -460,7 +613,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 template <int D>
 cudaError_t launch_tc(const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) {
   using C = TcCfg<D>;
-  TcArgs w{a, kTcRows / a.G};
+  TcArgs w{a, kTcRows / a.G, 0};
   auto fn = tma_encode_fn();
   if (!fn) return cudaErrorNotSupported;
   CUtensorMap qm, km, vm;
@@ -480,10 +633,15 @@ cudaError_t launch_tc(const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) 
   const long long items = a.kv.q_start ? (long long)a.T / pair + std::min(a.T, a.kv.n_seqs)
                                        : (long long)a.kv.n_seqs * ((a.kv.per + pair - 1) / pair);
   if (items * a.V > 0x7fffffffll) return cudaErrorInvalidValue;
+  // Clusters share the keys of an item where the items leave half of the SMs idle and the longest sequence gives every
+  // CTA two key tiles.
+  while (w.log_splits < 3 && (items * a.V << (w.log_splits + 1)) <= kAttnSms && a.kv.cap / kTcBK >= 4 << w.log_splits)
+    ++w.log_splits;
+  const unsigned splits = 1u << w.log_splits;
   const size_t smem = (size_t)C::kSmemTiles * C::kTileBytes + sizeof(TcBars<D>) + 1024;
   cudaError_t err = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  return launch_dependent(attn_tc_kernel<D>, (unsigned)(items * a.V), kTcThreads, smem, 1, s, qm, km, vm, w);
+  return launch_dependent(attn_tc_kernel<D>, (unsigned)(items * a.V) * splits, kTcThreads, smem, splits, s, qm, km, vm, w);
 }
 
 }  // namespace

@@ -37,23 +37,6 @@ struct NormArgs {
   uint32_t *status;
 };
 
-// (a0, a1) += (b0, b1) * (c0, c1), and (a0, a1) *= (b0, b1): one instruction for both, each lane rounded by itself.
-__device__ __forceinline__ void fma2(float &a0, float &a1, float b0, float b1, float c0, float c1) {
-  uint64_t acc, b, c;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(acc) : "f"(a0), "f"(a1));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(c0), "f"(c1));
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(b), "l"(c));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(acc));
-}
-__device__ __forceinline__ void mul2(float &a0, float &a1, float b0, float b1) {
-  uint64_t acc, b;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(acc) : "f"(a0), "f"(a1));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
-  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(b));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(acc));
-}
-
 template <int D>
 __global__ void __launch_bounds__(kNormThreads, 2) qk_norm_rope_kernel(const __grid_constant__ NormArgs a,
                                                                        const __grid_constant__ moe_rope rope) {
