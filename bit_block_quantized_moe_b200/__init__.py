@@ -41,3 +41,4 @@ from .binding import (  # noqa: F401
     moe_workspace_bytes,
 )
 from .layer import Q2MoeLayer  # noqa: F401
+from .decoder import PagedKvCache, Q2DecoderLayer  # noqa: F401

@@ -131,3 +131,31 @@ def test_rope_table():
                 want = theta ** (-2.0 * i / r) / (2 * math.pi) * 2.0 ** 64
                 assert abs(rope.turn[i] - want) <= 1 + want * 2.0 ** -50
             assert all(rope.turn[i] == 0 for i in range(r // 2, 64))
+
+
+def test_paged_cache_bookkeeping(lib):
+    import torch
+
+    from bit_block_quantized_moe_b200 import PagedKvCache
+
+    c = PagedKvCache(6, 4, 2, 64, 16, device="cpu")
+    assert c.k.shape == c.v.shape == (6, 2, 16, 64)
+    c.grow(3, 17)
+    c.grow(9, 1)
+    assert len(c.pages[3]) == 2 and len(c.pages[9]) == 1
+    first = list(c.pages[3])
+    c.grow(3, 32)
+    assert c.pages[3] == first
+    c.grow(3, 33)
+    assert c.pages[3][:2] == first and len(set(c.pages[3] + c.pages[9])) == 4
+    t = c.table([9, 3, 5])
+    assert t.dtype == torch.int32 and t.shape == (3, 3)
+    assert t[0, 1:].tolist() == [-1, -1] and t[1].tolist() == c.pages[3] and t[2].tolist() == [-1, -1, -1]
+    with pytest.raises(RuntimeError):
+        c.grow(5, 100)
+    c.release(3)
+    c.release(77)
+    c.grow(5, 80)
+    assert sorted(c.pages[5] + c.pages[9]) == list(range(6))
+    with pytest.raises(ValueError):
+        PagedKvCache(6, 4, 3, 64, 16, device="cpu")
