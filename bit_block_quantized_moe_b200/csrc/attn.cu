@@ -11,7 +11,9 @@
 // shares, one a CTA, whatever the lengths (they are read on the device, so that a captured graph follows them).
 // (Smaller shares taken as CTAs come free were slower: every share's ends cost more than the balance gave.)  A group
 // that is cut leaves parts (m, l, o) in the workspace; the CTA that brings the last one joins them in share order, so
-// that the result does not depend on which that is.
+// that the result does not depend on which that is.  Few groups over long caches have many parts each, too many for one
+// CTA to read: they are joined by a second launch, a CTA a row (one token at position 131072 of 2 key/value heads, 148
+// parts a head: 47.5 us with the join in one CTA).
 //   last warp  : walks the line; TMA of K and V, a page at a time, into a ring of stages (128-byte swizzle); a group's
 //                queries, and a record of where the stage stands, beside it;
 //   4 warps    : the scores of a quarter of the keys each, the weights to shared memory, then a quarter of the output's
@@ -30,6 +32,7 @@ namespace moe {
 namespace {
 
 constexpr float kWinLazy = 8.0f;
+constexpr int kJoinParts = 12;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -99,6 +102,7 @@ struct WinBars {
 struct WinArgs {
   AttnArgs a;
   int row_tiles;
+  int join_after;  // parts are joined by attn_join_kernel
 };
 
 // The key tiles of a sequence; one in which nothing is seen where it is empty.
@@ -634,7 +638,7 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
           if (warp == 0 && g == 0) __stcg(reinterpret_cast<float2 *>(pm + 2 * r), make_float2(m[i][e], sum));
         }
       }
-    if (c0 == c1) continue;
+    if (c0 == c1 || w.join_after) continue;
     // each share is the first of at most one cut group, whose count it keeps
     win_meet(false, kMeet);
     if (threadIdx.x == 0) {
@@ -700,6 +704,108 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
   }
 }
 
+// The parts of one row of a cut group, in share order: threads are D/4 pieces of four columns times kLanes, which take
+// every kLanes-th part each and are then summed in order.
+template <int D>
+__global__ void __launch_bounds__(512) attn_join_kernel(const __grid_constant__ WinArgs w, int tile_rows, int log_bk, int ctas) {
+  constexpr int kQuads = D / 4, kLanes = 512 / kQuads;
+  __shared__ float2 ml_s[kLanes];
+  __shared__ float4 o_s[kLanes][kQuads];
+  __shared__ long long total_s[17];
+  const AttnArgs &a = w.a;
+  const int groups = a.V * w.row_tiles, rows = a.kv.per * a.G;
+  const int r = blockIdx.x % tile_rows, group = blockIdx.x / tile_rows % groups, b = blockIdx.x / tile_rows / groups;
+  const int hv = group / w.row_tiles, rg = (group - hv * w.row_tiles) * tile_rows + r;
+  pdl_release();
+  pdl_wait();
+  if (rg >= rows) return;
+  // the line, and where this sequence stands in it
+  long long total = 0, line = 0;
+  for (int i = threadIdx.x; i < a.kv.n_seqs; i += 512) {
+    const int c = window_count(a, i, log_bk);
+    total += c;
+    if (i < b) line += c;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    line += __shfl_xor_sync(0xffffffffu, line, o);
+  }
+  __shared__ long long line_s[16];
+  if ((threadIdx.x & 31) == 0) {
+    total_s[threadIdx.x >> 5] = total;
+    line_s[threadIdx.x >> 5] = line;
+  }
+  __syncthreads();
+  total = line = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    total += total_s[i];
+    line += line_s[i];
+  }
+  total *= groups;
+  const int count = window_count(a, b, log_bk), shares = (int)min((long long)ctas, total);
+  const long long gs = line * groups + (long long)group * count, ge = gs + count;
+  const int c0 = share_of(gs, shares, total), c1 = share_of(ge - 1, shares, total);
+  if (c0 == c1) return;  // not cut
+  const int slot0 = gs > mul_div(total, c0, shares);
+  const size_t part = (size_t)tile_rows * (D + 2);
+  const int q = threadIdx.x % kQuads, lane = threadIdx.x / kQuads;
+  float m = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int k0 = c0 + lane; k0 <= c1; k0 += 8 * kLanes) {
+    float2 ml[8];
+    float4 v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int k = min(k0 + e * kLanes, c1);  // behind the last one, the last with no weight
+      const float *p = a.part + ((size_t)k * 2 + (k == c0 ? slot0 : 0)) * part;
+      ml[e] = __ldcg(reinterpret_cast<const float2 *>(p + (size_t)tile_rows * D + 2 * r));
+      v[e] = __ldcg(reinterpret_cast<const float4 *>(p + (size_t)r * D) + q);
+    }
+    float nm = m;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) nm = fmaxf(nm, ml[e].x);
+    const float sub = nm == -INFINITY ? 0.f : nm, f0 = ex2(m - sub);
+    m = nm;
+    l *= f0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] *= f0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (k0 + e * kLanes > c1) continue;
+      const float f = ex2(ml[e].x - sub);
+      l += ml[e].y * f;
+      y[0] += v[e].x * f;
+      y[1] += v[e].y * f;
+      y[2] += v[e].z * f;
+      y[3] += v[e].w * f;
+    }
+  }
+  if (q == 0) ml_s[lane] = make_float2(m, l);
+  o_s[lane][q] = make_float4(y[0], y[1], y[2], y[3]);
+  __syncthreads();
+  if (lane != 0) return;
+  float mm = -INFINITY, ll = 0.f, z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kLanes; ++i) mm = fmaxf(mm, ml_s[i].x);
+  const float sub = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+  for (int i = 0; i < kLanes; ++i) {
+    const float f = ex2(ml_s[i].x - sub);
+    const float4 v = o_s[i][q];
+    ll += ml_s[i].y * f;
+    z[0] += v.x * f;
+    z[1] += v.y * f;
+    z[2] += v.z * f;
+    z[3] += v.w * f;
+  }
+  const float inv = ll == 0.f ? 0.f : 1.0f / ll;
+  const int tok = rg / a.G;
+  uint16_t *dst = a.out + ((size_t)(b * a.kv.per + tok) * a.H + (size_t)hv * a.G + rg - tok * a.G) * D + 4 * q;
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(z[0] * inv, z[1] * inv), pack_bf16x2(z[2] * inv, z[3] * inv));
+}
+
 template <int D, int NR>
 cudaError_t launch(WinArgs w, const moe_kv_cache &c, cudaStream_t s) {
   using C = WinCfg<D, NR>;
@@ -709,7 +815,14 @@ cudaError_t launch(WinArgs w, const moe_kv_cache &c, cudaStream_t s) {
   w.row_tiles = (w.a.kv.per * w.a.G + C::kRows - 1) / C::kRows;
   cudaError_t err = cudaFuncSetAttribute(attn_window_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (err != cudaSuccess) return err;
-  return launch_dependent(attn_window_kernel<D, NR>, kAttnSms * C::kCtas, C::kThreads, C::kSmem, 1, s, km, vm, w);
+  // more than kJoinParts parts a group, were all sequences alike: the second launch
+  const int ctas = kAttnSms * C::kCtas;
+  const long long groups = (long long)w.a.kv.n_seqs * w.a.V * w.row_tiles;
+  w.join_after = groups * kJoinParts < ctas && w.a.kv.cap > kJoinParts * C::kBK;
+  err = launch_dependent(attn_window_kernel<D, NR>, ctas, C::kThreads, C::kSmem, 1, s, km, vm, w);
+  if (err == cudaSuccess && w.join_after)
+    err = launch_dependent(attn_join_kernel<D>, (unsigned)groups * C::kRows, 512, 0, 1, s, w, C::kRows, C::kLogBK, ctas);
+  return err;
 }
 
 // Rows of a window: one, two, four or eight 8-row tiles side by side; more rows than 64 walk the keys again.
@@ -745,7 +858,7 @@ size_t attn_part_bytes(const moe_attn_dims &d, int, int) {
 }
 
 cudaError_t launch_attn(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) {
-  WinArgs w{a, 1};
+  WinArgs w{a, 1, 0};
   trace_mark(MOE_KERNEL_ATTN, false, s);
   const bool window = !a.kv.q_start && a.kv.per <= 8;
   const cudaError_t err = !window             ? launch_attn_tc(d, a, c, s)
