@@ -33,6 +33,7 @@ namespace {
 
 constexpr float kWinLazy = 8.0f;
 constexpr int kJoinParts = 12;
+constexpr int kTcMinRows = 32;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -860,7 +861,8 @@ size_t attn_part_bytes(const moe_attn_dims &d, int, int) {
 cudaError_t launch_attn(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) {
   WinArgs w{a, 1, 0};
   trace_mark(MOE_KERNEL_ATTN, false, s);
-  const bool window = !a.kv.q_start && a.kv.per <= 8;
+  const int rows = a.kv.per * a.G;
+  const bool window = !a.kv.q_start && a.kv.per <= 8 && !(rows > kTcMinRows && (long long)a.kv.n_seqs * a.V * 8 >= kAttnSms / 2);
   const cudaError_t err = !window             ? launch_attn_tc(d, a, c, s)
                           : d.head_dim == 128 ? launch_d<128>(w, c, s)
                                               : launch_d<64>(w, c, s);
