@@ -16,7 +16,7 @@
 // parts a head: 47.5 us with the join in one CTA).
 //   last warp  : walks the line; TMA of K and V, a page at a time, into a ring of stages (128-byte swizzle); a group's
 //                queries, and a record of where the stage stands, beside it;
-//   4 warps    : the scores of a quarter of the keys each, the weights to shared memory, then a quarter of the output's
+//   4 warps    : (8 for more than 16 rows, in two groups with half of the rows each) the scores of a quarter of the keys each, the weights to shared memory, then a quarter of the output's
 //                columns each over all keys, so that a group's end needs no exchange but of the row sums.  The running
 //                maximum is left as it is until some score exceeds it by 8 (a factor of 256, which fp32 sums and bf16
 //                weights carry without loss), so that a tile needs one meeting of the warps, which also tells them
@@ -60,14 +60,15 @@ template <int D, int NR>
 struct WinCfg {
   static constexpr int kLogBK = D == 128 ? 6 : 7;   // keys a tile: 16 KB of K and of V
   static constexpr int kBK = 1 << kLogBK;
-  static constexpr int kWarps = 4;                  // beside the producer
+  static constexpr int kRG = NR <= 2 ? 1 : NR / 2;  // groups of four warps, each with its own rows
+  static constexpr int kNR = NR / kRG;              // 8-row tiles a warp
+  static constexpr int kWarps = 4 * kRG;            // beside the producer
   static constexpr int kThreads = (kWarps + 1) * 32;
   static constexpr int kMK = kBK / 64;              // 16-key tiles a warp
   static constexpr int kMD = D / 64;                // 16-column tiles of the output a warp
   static constexpr int kRows = 8 * NR;
-  static constexpr int kCtas = NR <= 4 ? 2 : 1;     // a SM
-  static constexpr int kStages = NR <= 2 ? 3 : NR == 4 ? 2 : 4;  // what the shared memory holds
-  static constexpr bool kQRegs = NR * D <= 512;     // the queries' fragments stay in registers
+  static constexpr int kCtas = NR <= 2 ? 2 : 1;     // a SM
+  static constexpr int kStages = NR <= 2 ? 3 : 4;   // what the shared memory holds
   static constexpr int kHalfBytes = kBK * 128;      // 64 columns of a tile, one swizzle row a key
   static constexpr int kTileBytes = kBK * D * 2;    // K or V of a stage
   static constexpr int kStageBytes = 2 * kTileBytes;
@@ -171,10 +172,10 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
   extern __shared__ __align__(1024) uint8_t win_smem[];
   __shared__ WinBars<C::kStages> B;
   __shared__ long long sum_s[C::kThreads / 32];
-  __shared__ __align__(16) float row_s[C::kRows][C::kWarps];  // maxima, or sums, of each row by warp
+  __shared__ __align__(16) float row_s[C::kRows][4];  // maxima, or sums, of each row by warp
   __shared__ __align__(16) uint16_t use_s[2][8];  // by turns: a warp may be one tile ahead
-  __shared__ uint8_t tok_s[NR == 8 ? 1024 : C::kRows];  // the token of each row
-  __shared__ __align__(4) uint16_t mask_s[C::kWarps][C::kRows];  // keys of a warp's 16 that each row sees
+  __shared__ uint8_t tok_s[NR == 4 ? 1024 : C::kRows];  // the token of each row
+  __shared__ __align__(4) uint16_t mask_s[C::kWarps][8 * C::kNR];  // keys of a warp's 16 that each row sees
   __shared__ int last_s;
   const AttnArgs &a = w.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -354,15 +355,16 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
     return;
   }
 
-  // ---- the other warps ----
+  // ---- the other warps: quarter wq of the keys and columns, rows rb on ----
+  const int wq = warp & 3, rb = (warp >> 2) * 8 * C::kNR;
   constexpr int kMeet = C::kWarps * 32;
   uint32_t phase = 0;
   int cs = 0, turn = 0;
-  uint32_t qf[C::kQRegs ? NR : 1][D / 16][2];
-  float o[C::kMD][NR][4], m[NR][2], l[NR][2];  // columns of the C fragment: rows 8 i + 2 c and one more
+  uint32_t qf[C::kNR][D / 16][2];
+  float o[C::kMD][C::kNR][4], m[C::kNR][2], l[C::kNR][2];  // columns of the C fragment: rows 8 i + 2 c and one more
   uint32_t qs = 0;                             // where the group's queries lie
   // lane offsets in a stage: 16 keys x 2 pieces of K for ldmatrix, 16 keys x 2 pieces of V for its transposed form
-  const int kr = 16 * C::kMK * warp + (lane & 15), vr = (lane & 7) + ((lane >> 4) << 3);
+  const int kr = 16 * C::kMK * wq + (lane & 15), vr = (lane & 7) + ((lane >> 4) << 3);
   const uint32_t koff = (uint32_t)(kr * 128 + (((lane >> 4) ^ (kr & 7)) << 4));
   const uint32_t voff = (uint32_t)(C::kTileBytes + vr * 128);
   for (;;) {
@@ -370,31 +372,29 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
     const TileRec &rec = B.rec[cs];
     const int flags = came ? rec.flags : kRecEnd;
     const uint32_t st = smem0 + (uint32_t)cs * C::kStageBytes, ps = smem0 + C::kPAt + (uint32_t)turn * C::kPBytes;
-    float sc[C::kMK][NR][4];  // keys g and g + 8 of a tile, rows 2 c and 2 c + 1
+    float sc[C::kMK][C::kNR][4];  // keys g and g + 8 of a tile, rows 2 c and 2 c + 1
     bool grow = flags & kRecEnd;
     if (!grow) {
       if (flags & kRecFirst) {
         qs = smem0 + C::kQAt + (uint32_t)rec.q * C::kQBytes;
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
+        for (int i = 0; i < C::kNR; ++i) {
 #pragma unroll
           for (int t = 0; t < C::kMD; ++t) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
           m[i][0] = m[i][1] = -INFINITY;
           l[i][0] = l[i][1] = 0.f;
-          if constexpr (C::kQRegs) {
-            const int r = 8 * i + (lane & 7);
+          const int r = rb + 8 * i + (lane & 7);
 #pragma unroll
-            for (int k = 0; k < D / 16; k += 2)
-              ldsm_x4(qs + (uint32_t)(r * kChunks + ((2 * k + (lane >> 3)) ^ (r & 7))) * 16u, qf[i][k][0], qf[i][k][1],
-                      qf[i][k + 1][0], qf[i][k + 1][1]);
-          }
+          for (int k = 0; k < D / 16; k += 2)
+            ldsm_x4(qs + (uint32_t)(r * kChunks + ((2 * k + (lane >> 3)) ^ (r & 7))) * 16u, qf[i][k][0], qf[i][k][1],
+                    qf[i][k + 1][0], qf[i][k + 1][1]);
         }
       }
       // ---- scores of this warp's keys
 #pragma unroll
       for (int t = 0; t < C::kMK; ++t) {
 #pragma unroll
-        for (int i = 0; i < NR; ++i) sc[t][i][0] = sc[t][i][1] = sc[t][i][2] = sc[t][i][3] = 0.f;
+        for (int i = 0; i < C::kNR; ++i) sc[t][i][0] = sc[t][i][1] = sc[t][i][2] = sc[t][i][3] = 0.f;
 #pragma unroll
         for (int k = 0; k < D / 16; k += 2) {
           uint32_t kf[2][4];
@@ -403,23 +403,13 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
             ldsm_x4((st + koff + (uint32_t)(t * 2048 + ((k + e) >> 2) * C::kHalfBytes)) ^ (uint32_t)(((k + e) & 3) << 5),
                     kf[e][0], kf[e][1], kf[e][2], kf[e][3]);
 #pragma unroll
-          for (int i = 0; i < NR; ++i) {
-            uint32_t b[4];
-            if constexpr (C::kQRegs) {
-              b[0] = qf[i][k][0];
-              b[1] = qf[i][k][1];
-              b[2] = qf[i][k + 1][0];
-              b[3] = qf[i][k + 1][1];
-            } else {
-              const int r = 8 * i + (lane & 7);
-              ldsm_x4(qs + (uint32_t)(r * kChunks + ((2 * k + (lane >> 3)) ^ (r & 7))) * 16u, b[0], b[1], b[2], b[3]);
-            }
-            mma_bf16_16816(sc[t][i], kf[0], b[0], b[1], sc[t][i]);
-            mma_bf16_16816(sc[t][i], kf[1], b[2], b[3], sc[t][i]);
+          for (int i = 0; i < C::kNR; ++i) {
+            mma_bf16_16816(sc[t][i], kf[0], qf[i][k][0], qf[i][k][1], sc[t][i]);
+            mma_bf16_16816(sc[t][i], kf[1], qf[i][k + 1][0], qf[i][k + 1][1], sc[t][i]);
           }
         }
 #pragma unroll
-        for (int i = 0; i < NR; ++i)
+        for (int i = 0; i < C::kNR; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[t][i][e] *= a.scale_log2;
       }
@@ -427,11 +417,11 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
         // which of the warp's keys some row sees, and of these the ones whose values are not finite: 0 * v is NaN
         // then, so that where rows differ in what they see such a key is left out of the product, and the rows that
         // see it become NaN
-        const int n = rec.n, j0 = rec.j0, base_pos = n - a.kv.per, r0 = rec.rt * C::kRows;
+        const int n = rec.n, j0 = rec.j0, base_pos = n - a.kv.per, r0 = rec.rt * C::kRows + rb;
 #pragma unroll
         for (int t = 0; t < C::kMK; ++t) {
           // lane and lane + 16 look at one key, half of its values each
-          const int k0 = 16 * (C::kMK * warp + t), kk = k0 + (lane & 15), j = j0 + kk;
+          const int k0 = 16 * (C::kMK * wq + t), kk = k0 + (lane & 15), j = j0 + kk;
           const bool live = j < n && (a.window <= 0 || base_pos - j < a.window || j < a.n_sinks) &&
                             !(rec.bad[kk >> 5] >> (kk & 31) & 1);
           bool bad = false;
@@ -446,9 +436,9 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
           const uint32_t lv = __ballot_sync(0xffffffffu, live) & 0xffffu;
           uint32_t bd = __ballot_sync(0xffffffffu, bad);
           bd = (bd | bd >> 16) & 0xffffu;
-          if (lane == 0) use_s[turn][C::kMK * warp + t] = (uint16_t)(lv & ~bd);
+          if (lane == 0 && warp < 4) use_s[turn][C::kMK * wq + t] = (uint16_t)(lv & ~bd);
 #pragma unroll
-          for (int r = lane; r < C::kRows; r += 32) {
+          for (int r = lane; r < 8 * C::kNR; r += 32) {
             const int hi = r0 + r < rows ? base_pos + tok_s[r0 + r] - (j0 + k0) : -1;  // keys up to hi,
             const int lo = a.window > 0 ? hi - a.window + 1 : 0;                       // from lo on
             const int sk = a.window > 0 ? a.n_sinks - (j0 + k0) : 0;                   // or below sk
@@ -456,7 +446,7 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
           }
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < NR; ++i) {
+          for (int i = 0; i < C::kNR; ++i) {
             // two rows' masks: this lane's keys are bits 0 and 8 of each after the shift
             const uint32_t both = *reinterpret_cast<const uint32_t *>(&mask_s[warp][8 * i + 2 * c]), v = both >> g;
             if (!(v & 1u)) sc[t][i][0] = -INFINITY;
@@ -474,16 +464,16 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
     }
     // ---- weights, with the maximum as it stands; once more when one has to grow.  (A loop, so that its code is there
     // once: a group's first tile always goes round twice.)
-    float sums[NR][2];
+    float sums[C::kNR][2];
     bool grown = false, out = false;
     for (;;) {
       if (!(flags & kRecEnd)) {
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
+        for (int i = 0; i < C::kNR; ++i) {
           if (grown) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float4 x = *reinterpret_cast<const float4 *>(&row_s[8 * i + 2 * c + e][0]);
+              const float4 x = *reinterpret_cast<const float4 *>(&row_s[rb + 8 * i + 2 * c + e][0]);
               const float nm = fmaxf(m[i][e], fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)));
               const float f = ex2(m[i][e] - (nm == -INFINITY ? 0.f : nm));
               m[i][e] = nm;
@@ -508,8 +498,8 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
               const float e0 = ex2(x - s0), e1 = ex2(y - s1);
               sum0 += e0;
               sum1 += e1;
-              const int key = 16 * (C::kMK * warp + t) + g + 8 * h;
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(ps + (uint32_t)((i * C::kBK + key) * 16 + 4 * c)),
+              const int key = 16 * (C::kMK * wq + t) + g + 8 * h;
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(ps + (uint32_t)(((rb >> 3) + i) * (C::kBK * 16) + key * 16 + 4 * c)),
                            "r"(pack_bf16x2(e0, e1))
                            : "memory");
             }
@@ -523,21 +513,21 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
       out = win_meet(!came, kMeet) || (flags & kRecEnd);  // all leave together when a wait has given up
       if (out) break;
 #pragma unroll
-      for (int i = 0; i < NR; ++i)
+      for (int i = 0; i < C::kNR; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float x = fmaxf(sc[0][i][e], sc[0][i][2 + e]);
           if constexpr (C::kMK == 2) x = fmaxf(x, fmaxf(sc[C::kMK - 1][i][e], sc[C::kMK - 1][i][2 + e]));
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-          if (g == 0) row_s[8 * i + 2 * c + e][warp] = x;
+          if (g == 0) row_s[rb + 8 * i + 2 * c + e][wq] = x;
         }
       win_meet(false, kMeet);
       grown = true;
     }
     if (out) break;
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
+    for (int i = 0; i < C::kNR; ++i) {
       l[i][0] += sums[i][0];
       l[i][1] += sums[i][1];
     }
@@ -549,7 +539,7 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int t = 0; t < C::kMD; ++t) {
-          const int ch = 2 * (C::kMD * warp + t) + ((lane >> 3) & 1);
+          const int ch = 2 * (C::kMD * wq + t) + ((lane >> 3) & 1);
           ldsm_x4_t(st + voff + (uint32_t)((k + e) * 2048 + (ch >> 3) * C::kHalfBytes + (((ch & 7) ^ (vr & 7)) << 4)),
                     vf[e][t][0], vf[e][t][1], vf[e][t][2], vf[e][t][3]);
         }
@@ -570,9 +560,9 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
         }
       }
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
+      for (int i = 0; i < C::kNR; ++i) {
         uint32_t b0, b1, b2, b3;
-        ldsm_x4_t(ps + (uint32_t)((i * C::kBK + 16 * k + lane) * 16), b0, b1, b2, b3);
+        ldsm_x4_t(ps + (uint32_t)(((rb >> 3) + i) * (C::kBK * 16) + (16 * k + lane) * 16), b0, b1, b2, b3);
 #pragma unroll
         for (int t = 0; t < C::kMD; ++t) {
           mma_bf16_16816(o[t][i], vf[0][t], b0, b1, o[t][i]);
@@ -601,23 +591,23 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
 
     // ---- the end of this CTA's part of the group: row sums over the warps, in warp order
 #pragma unroll
-    for (int i = 0; i < NR; ++i)
+    for (int i = 0; i < C::kNR; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float x = l[i][e];
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-        if (g == 0) row_s[8 * i + 2 * c + e][warp] = x;
+        if (g == 0) row_s[rb + 8 * i + 2 * c + e][wq] = x;
       }
     win_meet(false, kMeet);
     const int live = min(rows - r0, C::kRows);
     constexpr size_t kPart = (size_t)C::kRows * (D + 2);
     float *po = a.part + ((size_t)share * 2 + slot) * kPart, *pm = po + (size_t)C::kRows * D;
 #pragma unroll
-    for (int i = 0; i < NR; ++i)
+    for (int i = 0; i < C::kNR; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = 8 * i + 2 * c + e, col = 16 * C::kMD * warp + g;
+        const int r = rb + 8 * i + 2 * c + e, col = 16 * C::kMD * wq + g;
         if (r >= live) continue;
         const float4 x = *reinterpret_cast<const float4 *>(&row_s[r][0]);
         const float sum = (x.x + x.y) + (x.z + x.w);
@@ -636,7 +626,7 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
             __stcg(po + (size_t)r * D + col + 16 * t, o[t][i][e]);
             __stcg(po + (size_t)r * D + col + 16 * t + 8, o[t][i][2 + e]);
           }
-          if (warp == 0 && g == 0) __stcg(reinterpret_cast<float2 *>(pm + 2 * r), make_float2(m[i][e], sum));
+          if (wq == 0 && g == 0) __stcg(reinterpret_cast<float2 *>(pm + 2 * r), make_float2(m[i][e], sum));
         }
       }
     if (c0 == c1 || w.join_after) continue;
@@ -826,14 +816,13 @@ cudaError_t launch(WinArgs w, const moe_kv_cache &c, cudaStream_t s) {
   return err;
 }
 
-// Rows of a window: one, two, four or eight 8-row tiles side by side; more rows than 64 walk the keys again.
+// Rows of a window: one, two or four 8-row tiles side by side; more rows than 32 walk the keys again.
 template <int D>
 cudaError_t launch_d(const WinArgs &w, const moe_kv_cache &c, cudaStream_t s) {
   const int rows = w.a.kv.per * w.a.G;
   return rows <= 8    ? launch<D, 1>(w, c, s)
          : rows <= 16 ? launch<D, 2>(w, c, s)
-         : rows <= 32 ? launch<D, 4>(w, c, s)
-                      : launch<D, 8>(w, c, s);
+                      : launch<D, 4>(w, c, s);
 }
 
 }  // namespace
@@ -851,10 +840,9 @@ bool make_pages_map(CUtensorMap *map, const uint16_t *cache, int n_pages, const 
 }
 
 size_t attn_part_bytes(const moe_attn_dims &d, int, int) {
-  // of windows two parts a share (with more than 32 rows, one CTA a SM, there are half as many shares); of chunks one a
+  // of windows two parts a share (with more than 16 rows, one CTA a SM, there are half as many shares); of chunks one a
   // CTA of a cluster, with at most kAttnSms CTAs where there are clusters
-  const int rows = 8 * d.n_heads / d.n_kv_heads;  // the most rows of a window, then those of a CTA
-  const size_t windows = (size_t)kAttnShares * 2 * (rows <= 8 ? 8 : rows <= 16 ? 16 : 32) * (d.head_dim + 2) * 4;
+  const size_t windows = (size_t)kAttnShares * 2 * (8 * d.n_heads / d.n_kv_heads <= 8 ? 8 : 16) * (d.head_dim + 2) * 4;
   return std::max(windows, (size_t)kAttnSms * 256 * d.head_dim * 4);
 }
 
