@@ -16,11 +16,15 @@
 // parts a head: 47.5 us with the join in one CTA).
 //   last warp  : walks the line; TMA of K and V, a page at a time, into a ring of stages (128-byte swizzle); a group's
 //                queries, and a record of where the stage stands, beside it;
-//   4 warps    : (8 for more than 16 rows, in two groups with half of the rows each) the scores of a quarter of the keys each, the weights to shared memory, then a quarter of the output's
-//                columns each over all keys, so that a group's end needs no exchange but of the row sums.  The running
+//   4 warps    : the scores of a quarter of the keys each, the weights to shared memory, then a quarter of the output's
+//                columns each over all keys, so that a group's end needs no exchange but of the row sums (8 warps for
+//                more than 16 rows, in two groups with half of the rows each; one group of four with all of them took
+//                86 us for 32 x 3 tokens at 8192, this 72.5).  The running
 //                maximum is left as it is until some score exceeds it by 8 (a factor of 256, which fp32 sums and bf16
 //                weights carry without loss), so that a tile needs one meeting of the warps, which also tells them
-//                whether it is so.  Two CTAs a SM: one computes while the other waits.
+//                whether it is so.  Two CTAs a SM (of 4 warps): one computes while the other waits.
+// Bound: HBM; 64 ragged sequences of up to 16384 tokens (0.55 GB of keys and values) take 92 us, 93% of the copy rate.
+// Short calls are chains of waits: 500 tokens of one sequence 8 us.
 // Values of keys that no query of the window sees are masked in the registers that feed the product, so that nothing
 // behind them can reach an output.  Every wait is bounded (sync.cuh).
 #include <algorithm>
@@ -32,7 +36,10 @@ namespace moe {
 namespace {
 
 constexpr float kWinLazy = 8.0f;
-constexpr int kJoinParts = 12;
+constexpr int kJoinParts = 12;  // more parts a group go to the second launch (4: 7 sequences 36 us instead of 25)
+// Windows of more rows go to the chunk kernel's tiles where they fill the SMs: 32 x 8 tokens of 8 heads a group at 8192
+// 66 us there, 131 here; 32 x 3 tokens 65 and 73, but 64 ragged sequences 216 and 135, as a chunk tile walks a whole
+// sequence, and so up to 32 rows stay.
 constexpr int kTcMinRows = 32;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
@@ -850,7 +857,8 @@ cudaError_t launch_attn(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_
   WinArgs w{a, 1, 0};
   trace_mark(MOE_KERNEL_ATTN, false, s);
   const int rows = a.kv.per * a.G;
-  const bool window = !a.kv.q_start && a.kv.per <= 8 && !(rows > kTcMinRows && (long long)a.kv.n_seqs * a.V * 8 >= kAttnSms / 2);
+  const bool fills = (long long)a.kv.n_seqs * a.V * 8 >= kAttnSms / 2;  // with clusters of 8
+  const bool window = !a.kv.q_start && a.kv.per <= 8 && !(rows > kTcMinRows && fills);
   const cudaError_t err = !window             ? launch_attn_tc(d, a, c, s)
                           : d.head_dim == 128 ? launch_d<128>(w, c, s)
                                               : launch_d<64>(w, c, s);

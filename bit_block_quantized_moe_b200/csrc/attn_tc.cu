@@ -6,7 +6,11 @@
 //   S_i = Q_i K_j^T            (tensor memory, fp32)
 //   P_i = 2^(scale S_i - m)    (one thread a row; bf16, over S_i in tensor memory)
 //   O_i += P_i V_j             (tensor memory, fp32)
-// The products of one row tile run under the softmax of the other.  m is the maximum seen so far, left as it is
+// The products of one row tile run under the softmax of the other.  A tile's chain of softmax (2300 cycles), P V and the
+// next Q K (700 and 620) paces it: 8192 tokens of 16 heads over 2 key/value heads take 252 us, 1095 TFLOP/s, with the
+// tensor core busy two thirds of the time.  Slower: two threads a row (309 us, the exchange of the halves' maxima), a
+// quarter or half of the exponentials as polynomials on the FMA units (264, 302: the special function unit is not the
+// limit), weights begun before the maximum is known (262).  m is the maximum seen so far, left as it is
 // until a row exceeds it by 8 (a factor of 256, which fp32 sums and bf16 weights carry without loss: only then are l
 // and O_i, which lie in tensor memory, rescaled), so that the rescaling is rare.
 //   warps 0-3, 4-7 : softmax of row tile 0, 1, then its output rows;
@@ -31,6 +35,7 @@ constexpr int kTcRows = 128;
 constexpr int kTcThreads = 384;
 constexpr int kTcInfo = 8;   // ring of tile descriptions: more than the tiles between the producer and a softmax
 constexpr float kTcLazy = 8.0f;
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // of a thread: 256 x 216 + 128 x 72 are the launch's 384 x 168
 
 template <int D>
 struct TcCfg {
@@ -229,9 +234,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t tbase = B.tmem;
   float m = -INFINITY, l = 0.f;  // of a row, in its softmax thread: m in units of log2, scaled
 
-  // Registers go from the last four warps to the softmax: 256 x 216 + 128 x 72 are the launch's 384 x 168.
+  // Registers go from the last four warps to the softmax.
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 8) {
     // ---- producer ----
     const int rows = w.tokens * a.G;
@@ -391,7 +396,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     cluster_meet();
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax of row tile i: one thread a row ----
     const int i = warp >> 2, row = threadIdx.x & 127;
     if (i < nq) {
@@ -638,8 +643,13 @@ cudaError_t launch_tc(const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) 
   while (w.log_splits < 3 && (items * a.V << (w.log_splits + 1)) <= kAttnSms && a.kv.cap / kTcBK >= 4 << w.log_splits)
     ++w.log_splits;
   const unsigned splits = 1u << w.log_splits;
+  // the register shares have to be what the launch holds: raising them waits for what the others give up
+  cudaFuncAttributes fa;
+  cudaError_t err = cudaFuncGetAttributes(&fa, attn_tc_kernel<D>);
+  if (err != cudaSuccess) return err;
+  if (fa.numRegs * kTcThreads < 2 * 128 * kSoftmaxRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
   const size_t smem = (size_t)C::kSmemTiles * C::kTileBytes + sizeof(TcBars<D>) + 1024;
-  cudaError_t err = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  err = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   return launch_dependent(attn_tc_kernel<D>, (unsigned)(items * a.V) * splits, kTcThreads, smem, splits, s, qm, km, vm, w);
 }

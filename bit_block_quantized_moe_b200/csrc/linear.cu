@@ -7,17 +7,19 @@
 //                    past the end and columns past K read as zeros);
 //   MMA warp       : 4 tcgen05.mma per chunk, both operands in shared memory; two accumulators in tensor memory, so
 //                    that a tile's epilogue runs under the next tile's products;
-// Many tiles go to pairs of CTAs (tcgen05 cta_group::2): a pair's tile is 256 features x BN tokens, each CTA holds 128
-// weight rows, half of the token rows and the sums of its own features, and the first of them issues the products for
-// both.  What a SM has to fetch through L2 per product, which bounds the single-CTA form (85 bytes a nanosecond a SM),
-// falls by a third.
 //   epilogue warps : tensor memory lane quadrant = warp & 3; with 8 of them each has half of the columns.
+// Many tiles of more than 128 features go to pairs of CTAs (tcgen05 cta_group::2): a pair's tile is 256 features x BN
+// tokens, each CTA holds 128 weight rows, half of the token rows and the sums of its own features, and the first of
+// them issues the products for both.  What a SM has to fetch through L2 per product, which bounds the single-CTA form
+// (85 bytes a nanosecond a SM), falls by a third.
 // With an fp32 output K runs in slices of 512: each slice has a fresh accumulator, added in fp32 to a running sum in
 // the epilogue's registers, because the tensor core's long accumulation truncates: without a residual K = 2048 is
 // 2.1e-6 of the result off and K = 4096 4.4e-6, which bf16 hides and fp32 does not; in slices of 512 it is 4.7e-7 at
-// any K (an fp32 product in software: 3.9e-7 and 6.1e-7), in slices of 256 2.4e-7 but 14% slower.  When the tiles alone leave SMs idle, a cluster of 2, 4 or 8 CTAs
-// splits K: each sends the others their features' parts through distributed shared memory and finishes its own,
-// summed in rank order.  Every wait is bounded (sync.cuh).
+// any K (an fp32 product in software: 3.9e-7 and 6.1e-7), in slices of 256 2.4e-7 but 14% slower.
+// When the tiles alone leave SMs idle, a cluster of 2, 4 or 8 CTAs splits K: each sends the others their features'
+// parts through distributed shared memory and finishes its own, summed in rank order.  Every wait is bounded (sync.cuh).
+// Measured: 32768 x 2048 x 2560 231 us (1490 TFLOP/s; single CTAs 311); 1024 x 2048 x 2048 onto the residual 15.4 us,
+// of which 7 are launch, first loads and epilogue; 3 x 2048 x 2560 5.7 us against 1.6 for reading the weights.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -40,7 +42,7 @@ struct LnCfg {
   static constexpr int kABytes = kLnM * kLnK * 2;
   static constexpr int kBBytes = BN * kLnK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = SPLIT ? (BN >= 128 ? 4 : BN == 64 ? 5 : 4) : BN == 256 ? 4 : 6;
+  static constexpr int kStages = SPLIT ? (BN == 64 ? 5 : 4) : BN == 256 ? 4 : 6;
   static constexpr int kSumBytes = SPLIT ? kLnM * BN * 4 : 0;  // the cluster's parts of this CTA's features
   static constexpr uint32_t kTmemCols = 2 * BN;
   static constexpr int kSumAt = kStages * kStageBytes;
@@ -565,8 +567,9 @@ cudaError_t launch_linear(const uint16_t *x, int64_t ld, const uint16_t *w, cons
   a.resid = resid;
   a.out = out;
   a.status = status;
-  // The tile that takes the fewest rounds of 64-wide chunks, each weighed by its products' cycles; where the tiles
-  // would leave more than half of the SMs idle, K split over a cluster.
+  // The tile that takes the fewest rounds of 64-wide chunks, each weighed by its products' cycles (64 columns are bound
+  // by shared memory, 192 cycles); where the tiles leave half of the SMs idle, K split over a cluster (3 x 2048 x 2560:
+  // 7.4 us with the parts through global memory and a second launch, 6.5 so; 777 x 1160 x 1001 17.4 and 14.6).
   auto tiles = [&](int bn) { return (long long)a.n_ft * ((T + bn - 1) / bn); };
   int bn = 16;
   if (T > 16) {
@@ -584,9 +587,9 @@ cudaError_t launch_linear(const uint16_t *x, int64_t ld, const uint16_t *w, cons
   }
   a.ks = 1;
   a.slice = resid ? kLnSliceChunks : a.chunks;
-  // pairs of CTAs, once their tiles fill most of the SMs
+  // Pairs of CTAs, once their tiles fill three quarters of the SMs.
   const int n_ft2 = (N + 255) / 256, pair = resid ? 128 : 256;
-  for (int c = pair; c >= 128; c /= 2) {
+  for (int c = pair; c >= 128 && N > kLnM; c /= 2) {
     const long long t = (long long)n_ft2 * ((T + c - 1) / c);
     if (t * 4 < kLnWave / 2 * 3) continue;
     if (t > 0x7fffffffll) return cudaErrorInvalidValue;
@@ -597,14 +600,14 @@ cudaError_t launch_linear(const uint16_t *x, int64_t ld, const uint16_t *w, cons
     trace_mark(MOE_KERNEL_LINEAR, true, s);
     return err;
   }
-  while (bn <= 128 && a.ks < 8 && tiles(bn) * a.ks * 2 <= (bn == 16 ? 2 : 1) * kLnWave && a.chunks / (a.ks * 2) >= 2) a.ks *= 2;
+  while (bn <= 64 && a.ks < 8 && tiles(bn) * a.ks * 2 <= (bn == 16 ? 2 : 1) * kLnWave && a.chunks / (a.ks * 2) >= 2) a.ks *= 2;
   const long long units = tiles(bn) * a.ks;
   if (units > 0x7fffffffll) return cudaErrorInvalidValue;
   a.n_units = (int)units;
   trace_mark(MOE_KERNEL_LINEAR, false, s);
   cudaError_t err;
   if (a.ks > 1)
-    err = bn == 16 ? launch<16, true>(x, ld, w, K, a, s) : bn == 64 ? launch<64, true>(x, ld, w, K, a, s) : launch<128, true>(x, ld, w, K, a, s);
+    err = bn == 16 ? launch<16, true>(x, ld, w, K, a, s) : launch<64, true>(x, ld, w, K, a, s);
   else
     err = bn == 16    ? launch<16, false>(x, ld, w, K, a, s)
           : bn == 64  ? launch<64, false>(x, ld, w, K, a, s)

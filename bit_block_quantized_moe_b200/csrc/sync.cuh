@@ -192,7 +192,9 @@ inline cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigne
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (err != cudaSuccess) cudaGetLastError();  // reported here, not by the next launch
+  return err;
 }
 
 }  // namespace moe

@@ -389,9 +389,10 @@ moe_status moe_qk_norm_rope(const moe_attn_dims *dims, const uint16_t *qkv, int6
  * What lies in cache rows that a query does not see (any bits, NaN among them) does not
  * reach its output; a non-finite v that it sees may make its whole output row NaN.
  * window = 0: all earlier tokens; n_sinks >= 0 (without a window it changes nothing).
- * Which kernel runs: q_start == NULL and T <= 8 n_seqs (verify windows) splits each
- * sequence's cached length over the SMs and joins the parts; anything else (prompt
- * chunks) takes tiles of queries. */
+ * Which kernel runs: q_start == NULL and T <= 8 n_seqs (verify windows) splits the
+ * cached lengths evenly over the SMs and joins the parts; anything else (prompt
+ * chunks), and windows of more than 32 rows (new tokens x group) where these fill
+ * the SMs, takes tiles of queries. */
 moe_status moe_attn_forward(const moe_attn_dims *dims, const uint16_t *q, int64_t ld_q, const moe_kv_cache *cache,
                             const moe_kv_batch *batch, int32_t T, float scale, int32_t window, int32_t n_sinks,
                             uint16_t *out, void *workspace, size_t ws_bytes, moe_stream_t stream);

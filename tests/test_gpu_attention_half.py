@@ -69,7 +69,10 @@ LINEAR = [(1, 8, 1, "none", False, False), (1, 2048, 2560, "none", True, False),
           (65, 136, 1001, "silu", True, False), (300, 2048, 257, "none", True, True),
           (129, 1160, 384, "gelu", False, True), (777, 1160, 1001, "silu", True, False),
           (1024, 2048, 2048, "none", False, True), (2500, 520, 640, "gelu", True, False),
-          (5000, 256, 72, "silu", False, True), (4, 65536, 40, "none", False, False)]
+          (5000, 256, 72, "silu", False, True), (4, 65536, 40, "none", False, False),
+          (4000, 200, 1100, "silu", True, False), (4000, 1096, 1100, "none", True, True),
+          (40000, 64, 100, "none", True, False), (20000, 1160, 100, "gelu", False, True),
+          (16, 136, 20000, "none", True, False), (9, 2048, 300, "gelu", True, True)]
 
 
 @pytest.mark.parametrize("T,K,N,act,has_bias,has_resid", LINEAR)
@@ -221,7 +224,11 @@ WINDOWS = [  # H, V, D, page, new, totals, window, sinks
     (128, 1, 128, 16, 2, [400, 1500], 0, 0),
     (6, 2, 128, 64, 1, [20000, 1, 3], 0, 0),
     (4, 2, 64, 32, 2, [64 + 31] * 70, 50, 1),
-    (24, 8, 128, 64, 1, [9000], 4096, 4),
+    (32, 8, 128, 64, 1, [9000], 4096, 4),
+    (16, 2, 128, 64, 8, [1000, 8, 70, 9, 2000, 300], 0, 0),   # more rows than a window's tiles: the chunk kernel
+    (40, 4, 64, 16, 7, [500, 7, 1200], 100, 2),
+    (16, 2, 128, 64, 3, [70000], 0, 0),                       # many parts of few groups
+    (80, 2, 128, 64, 5, [6000], 0, 0),
 ]
 
 
@@ -246,6 +253,10 @@ CHUNKS = [  # H, V, D, page, new, totals, window, sinks
     (2, 1, 128, 64, [1000], [1500], 1, 0),
     (8, 2, 128, 64, [1024], [1024], 0, 0),
     (3, 3, 128, 64, [600, 600], [600, 2000], 1000, 1),
+    (16, 2, 128, 64, [16], [9000], 0, 0),
+    (8, 2, 64, 16, [200], [5000], 0, 0),
+    (20, 1, 128, 32, [11, 40], [4000, 60], 0, 0),
+    (6, 1, 64, 128, [12, 9, 30], [12, 3000, 900], 700, 9),
 ]
 
 
@@ -384,20 +395,20 @@ def test_attention_offsets_beyond_32_bits(M, new):
     g = gen(12)
     V, ps, D = 8, 128, 128
     n_pages = 2300000000 // (V * ps * D)
-    dims = M.moe_attn_dims(8, V, D, ps)
+    dims = M.moe_attn_dims(16, V, D, ps)
     k = torch.empty((n_pages, V, ps, D), dtype=torch.bfloat16, device="cuda")
     v = torch.empty_like(k)
-    small = Batch(M, g, 8, V, D, ps, [new], [500])
+    small = Batch(M, g, 16, V, D, ps, [new], [500])
     last = torch.arange(n_pages - small.k.shape[0], n_pages, device="cuda")
     k[last], v[last] = small.k, small.v
-    q = normal(g, new, 8, D).bfloat16()
+    q = normal(g, new, 16, D).bfloat16()
     out = torch.empty_like(q)
     M.moe_attn_forward(dims, q, out, k, v, small.kv_len, small.table + int(last[0]), small.ws)
     M.moe_check_status(small.ws)
     ref, tol = attend64(small, q, 0, 0)
     assert ((out.double() - ref).abs() <= tol).all()
     # and the rows that the norm writes there
-    qkv = normal(g, new, 24 * D).bfloat16()
+    qkv = normal(g, new, 32 * D).bfloat16()
     M.moe_qk_norm_rope(dims, qkv, out, k, v, small.kv_len, small.table + int(last[0]), small.ws)
     M.moe_qk_norm_rope(dims, qkv, torch.empty_like(out), small.k, small.v, small.kv_len, small.table, small.ws)
     assert torch.equal(k[last], small.k) and torch.equal(v[last], small.v)
