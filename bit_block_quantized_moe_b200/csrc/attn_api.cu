@@ -19,7 +19,7 @@ constexpr size_t kWsCounts = 256;
 static_assert(kWsCounts + kAttnShares * 4 <= kWsHeader, "the counts lie in the header");
 
 static bool linear_dims_ok(int32_t T, int32_t K, int32_t N) {
-  return T >= 0 && K >= 8 && K <= 65536 && K % 8 == 0 && N >= 1 && N <= 262144;
+  return T >= 0 && T <= (1 << 30) && K >= 8 && K <= 65536 && K % 8 == 0 && N >= 1 && N <= 262144;
 }
 
 static bool attn_dims_ok(const moe_attn_dims *d) {
@@ -141,7 +141,8 @@ moe_status moe_qk_norm_rope(const moe_attn_dims *dims, const uint16_t *qkv, int6
 moe_status moe_attn_forward(const moe_attn_dims *dims, const uint16_t *q, int64_t ld_q, const moe_kv_cache *cache,
                             const moe_kv_batch *batch, int32_t T, float scale, int32_t window, int32_t n_sinks,
                             uint16_t *out, void *workspace, size_t ws_bytes, moe_stream_t stream) {
-  if (!attn_dims_ok(dims) || T < 0 || window < 0 || n_sinks < 0 || !isfinite(scale * 1.4426950408889634f)) return MOE_ERR_ARG;
+  if (!attn_dims_ok(dims) || T < 0 || window < 0 || n_sinks < 0) return MOE_ERR_ARG;
+  if (!isfinite(scale * 1.4426950408889634f)) return MOE_ERR_ARG;
   if (T == 0) return MOE_OK;
   if (!q || !out || !workspace) return MOE_ERR_ARG;
   AttnArgs a{};

@@ -67,11 +67,17 @@ class Q2DecoderLayer:
         self.rope = B.moe_rope_init(rope_theta, d.head_dim if rotary_dim is None else rotary_dim)
         self.window, self.n_sinks = window, n_sinks
         self._reserved = (-1, -1)
+        self._captured, self._kept = False, []
 
     def reserve(self, T: int, n_seqs: int):
-        """Activations and workspace for calls of up to T tokens and n_seqs sequences."""
+        """Activations and workspace for calls of up to T tokens and n_seqs sequences, as for Q2MoeLayer shared by all
+        calls of this layer: two that can run at the same time need a layer each."""
         if T <= self._reserved[0] and n_seqs <= self._reserved[1]:
             return
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("reserve the largest call before capturing one")
+        if self._captured:  # a graph that still reads and writes the smaller buffers
+            self._kept.append((self._qkv, self._q, self._o, self._mid, self._ws, self.moe.workspace))
         T, n_seqs = max(T, self._reserved[0]), max(n_seqs, self._reserved[1])
         d, hidden, dev = self.cache.dims, self.moe.dims.hidden, self.moe.device
         rows = lambda n: torch.empty((T, n), dtype=torch.bfloat16, device=dev)  # noqa: E731
@@ -93,6 +99,7 @@ class Q2DecoderLayer:
         if T == 0:
             return x_norm_out
         self.reserve(T, kv_len.shape[0])
+        self._captured = self._captured or torch.cuda.is_current_stream_capturing()
         c, ws = self.cache, self._ws
         x = x_norm if x_norm.dtype == torch.bfloat16 else x_norm.view(torch.bfloat16)
         qkv, q, o, mid = self._qkv[:T], self._q[:T], self._o[:T], self._mid[:T]

@@ -302,8 +302,8 @@ moe_status moe_rmsnorm_residual(float *resid, const uint16_t *y, uint16_t *x_nor
  * x [T, K] bf16 with ld_x elements between rows, w [N, K] bf16 row-major, bias [N]
  * fp32 or NULL, resid [T, N] fp32.  silu(z) = z / (1 + exp(-z)), gelu(z) =
  * z/2 (1 + erf(z / sqrt 2)).  K and ld_x are multiples of 8, 8 <= K <= 65536,
- * 1 <= N <= 262144, ld_x >= K; x, w, bias, resid and out 16-byte aligned.  Out may not overlap
- * x, w or bias.  T = 0 is a no-op. */
+ * 1 <= N <= 262144, ld_x >= K, T <= 2^30; x, w, bias, resid and out 16-byte aligned.
+ * Out may not overlap x, w or bias.  T = 0 is a no-op. */
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2 } moe_act;
 /* Host.  Workspace bytes of moe_linear for every T <= max_T (0 if invalid). */
 size_t moe_linear_workspace_bytes(int32_t max_T, int32_t K, int32_t N);

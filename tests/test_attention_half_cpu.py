@@ -38,7 +38,7 @@ def test_linear_refusals(lib):
         return lib.moe_linear(x, ld, w, bias, act, resid, out, T, K, N, wsp, wsb, None)
 
     assert call(T=0) == 0
-    for bad in (dict(T=-1), dict(K=0), dict(K=4), dict(K=250), dict(K=65544), dict(N=0), dict(N=262145), dict(act=3),
+    for bad in (dict(T=-1), dict(T=(1 << 30) + 1), dict(K=0), dict(K=4), dict(K=250), dict(K=65544), dict(N=0), dict(N=262145), dict(act=3),
                 dict(act=-1), dict(x=None), dict(w=None), dict(out=None), dict(wsp=None), dict(ld=248), dict(ld=260),
                 dict(out=0x100000 + 4096), dict(out=0x200000), dict(out=0x300000 - 16),
                 dict(resid=0x400000 + 16), dict(resid=0x400000 - 64)):

@@ -229,6 +229,7 @@ WINDOWS = [  # H, V, D, page, new, totals, window, sinks
     (40, 4, 64, 16, 7, [500, 7, 1200], 100, 2),
     (16, 2, 128, 64, 3, [70000], 0, 0),                       # many parts of few groups
     (80, 2, 128, 64, 5, [6000], 0, 0),
+    (4, 2, 64, 16, 1, [1 + 7 * i % 90 for i in range(900)], 0, 0),
 ]
 
 
@@ -257,6 +258,7 @@ CHUNKS = [  # H, V, D, page, new, totals, window, sinks
     (8, 2, 64, 16, [200], [5000], 0, 0),
     (20, 1, 128, 32, [11, 40], [4000, 60], 0, 0),
     (6, 1, 64, 128, [12, 9, 30], [12, 3000, 900], 700, 9),
+    (4, 1, 64, 16, [i % 11 for i in range(700)], [i % 11 + i % 70 for i in range(700)], 0, 0),
 ]
 
 

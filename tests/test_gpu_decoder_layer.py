@@ -169,6 +169,48 @@ def test_windows_replayed_from_a_graph(M):
     layer.check_status()
 
 
+def test_a_graph_outlives_the_buffers_of_its_call(M, monkeypatch):
+    """A larger eager call makes larger buffers; the graph captured before it still owns its own."""
+    layer = build(M)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    hidden = layer.moe.dims.hidden
+    layer.cache.grow(0, 30)
+    layer.cache.grow(1, 500)
+    layer.cache.k.normal_(generator=g)
+    layer.cache.v.normal_(generator=g)
+    one, long = layer.cache.table([0]), layer.cache.table([1])
+    start = torch.randn((1, hidden), generator=g, device="cuda")
+    resid, x_next = start.clone(), torch.empty((1, hidden), dtype=torch.bfloat16, device="cuda")
+    x = torch.empty_like(x_next)
+    kv_len = torch.tensor([30], dtype=torch.int32, device="cuda")
+
+    def step():
+        M.moe_rmsnorm_residual(resid, None, x, 1, hidden, EPS)
+        layer.forward(x, resid, x_next, kv_len, one)
+
+    step()
+    want = resid.clone(), x_next.clone()
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+        with pytest.raises(RuntimeError, match="reserve"):
+            layer.reserve(9, 1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    many = torch.randn((400, hidden), generator=g, device="cuda")
+    x_many = torch.empty((400, hidden), dtype=torch.bfloat16, device="cuda")
+    M.moe_rmsnorm_residual(many, None, x_many, 400, hidden, EPS)
+    layer.forward(x_many, many, torch.empty_like(x_many), torch.tensor([500], dtype=torch.int32, device="cuda"), long)
+    held = [torch.full((400, hidden), 7.0, device="cuda") for _ in range(64)]  # takes what the allocator has free
+    resid.copy_(start)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(resid, want[0]) and torch.equal(x_next, want[1])
+    assert all((h == 7.0).all() for h in held)
+    layer.check_status()
+
+
 def test_padding_rows_keep_their_residual_until_the_moe_half(M):
     layer = build(M)
     g = torch.Generator(device="cuda").manual_seed(7)
