@@ -848,9 +848,9 @@ bool make_pages_map(CUtensorMap *map, const uint16_t *cache, int n_pages, const 
 
 size_t attn_part_bytes(const moe_attn_dims &d, int, int) {
   // of windows two parts a share (with more than 16 rows, one CTA a SM, there are half as many shares); of chunks one a
-  // CTA of a cluster, with at most kAttnSms CTAs where there are clusters
+  // CTA that shares an item, of which there are at most kAttnSms, with its rows' maxima and sums and the items' rows
   const size_t windows = (size_t)kAttnShares * 2 * (8 * d.n_heads / d.n_kv_heads <= 8 ? 8 : 16) * (d.head_dim + 2) * 4;
-  return std::max(windows, (size_t)kAttnSms * 256 * d.head_dim * 4);
+  return std::max(windows, (size_t)kAttnSms * (256 * (d.head_dim * 4 + 8) + 8));
 }
 
 cudaError_t launch_attn(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) {

@@ -70,6 +70,9 @@ struct TcArgs {
   AttnArgs a;
   int tokens;  // tokens a row tile: 128 / G
   int log_splits;  // log2 of the CTAs of a cluster, which share an item's key tiles
+  int parts;       // else the CTAs that share them without a cluster, joined by a second launch; or 0
+  float2 *ml;      // [CTAs, 256] maximum and sum of each row of the parts
+  int2 *rows;      // [items x V] first row and number of tokens of an item
 };
 
 template <class Bars>
@@ -108,26 +111,27 @@ struct TcRows {
   int H, G, tok0, tokens, m, nq;
 };
 
-// The rows of one CTA of a cluster of 2^LS: row k * 2^LS + split for k = first, first + step, ..., all parts of all rows
-// of a lane in flight at once.  `mine`: this CTA's part in shared memory; `parts`: the others'.
+// The rows of one CTA of a cluster of 2^LS: row own * split + k for k = first, first + step, ..., all parts of all rows
+// of a lane in flight at once.  `mine`: this CTA's part in shared memory; `parts`: the others', in the same layout.
 template <int D, int LS>
 __device__ __forceinline__ void tc_join(const TcRows &w, const float2 *ml, const uint8_t *tok, const float *mine,
                                         const float *parts, int split, int first, int sub) {
   constexpr int kQuads = D / 4, kStep = 8 * (32 / kQuads), kOwn = 256 >> LS, kRows = kOwn / kStep, kParts = 1 << LS;
+  const int own = w.nq * 128 >> LS;
   float4 o[kRows][kParts];
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
-    const int r = ((first + u * kStep) << LS) + split, q = min(r, w.nq * 128 - kParts + split);  // rows that are there
+    const int q = own * split + min(first + u * kStep, own - 1), piece = (sub ^ (q & (kQuads - 1))) << 2;
 #pragma unroll
     for (int p = 0; p < kParts; ++p)
-      o[u][p] = p == split ? *reinterpret_cast<const float4 *>(mine + (size_t)q * D + ((sub ^ (q & (kQuads - 1))) << 2))
-                           : __ldcg(reinterpret_cast<const float4 *>(parts + ((size_t)p * 256 + q) * D) + sub);
+      o[u][p] = p == split ? *reinterpret_cast<const float4 *>(mine + (size_t)q * D + piece)
+                           : __ldcg(reinterpret_cast<const float4 *>(parts + ((size_t)p * 256 + q) * D + piece));
   }
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
-    const int k = first + u * kStep, r = (k << LS) + split, i = r >> 7, rt = tok[r & 127];
+    const int k = first + u * kStep, r = own * split + k, i = r >> 7, rt = tok[r & 127];
     const int tk = w.tok0 + i * w.tokens + rt;
-    if (i >= w.nq || rt >= w.tokens || tk >= w.m) continue;
+    if (k >= own || rt >= w.tokens || tk >= w.m) continue;
     float mx = -INFINITY;
 #pragma unroll
     for (int p = 0; p < kParts; ++p) mx = fmaxf(mx, ml[p * kOwn + k].x);
@@ -160,13 +164,38 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   TcBars<D> &B = *reinterpret_cast<TcBars<D> *>(smem + C::kSmemTiles * C::kTileBytes);
   const AttnArgs &a = w.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int splits = 1 << w.log_splits, split = blockIdx.x & (splits - 1), unit = blockIdx.x >> w.log_splits, hv = unit % a.V, item = unit / a.V;
+  const int splits = w.parts ? w.parts : 1 << w.log_splits;
+  const int unit = w.parts ? blockIdx.x / w.parts : blockIdx.x >> w.log_splits, split = blockIdx.x - unit * splits;
+  const int hv = unit % a.V, item = unit / a.V;
   pdl_release();
+  // what needs no memory that others write
+  if (threadIdx.x < 128) B.tok[threadIdx.x] = (uint8_t)min((int)threadIdx.x / a.G, w.tokens);
+  if (threadIdx.x == 0) {
+    mbar_init(&B.q_full, 1);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&B.k_full[i], 1);
+      mbar_init(&B.k_empty[i], 1);
+      mbar_init(&B.v_full[i], 1);
+      mbar_init(&B.v_ready[i], 2);
+      mbar_init(&B.v_empty[i], 3);  // the products' commit and the two clearing warps
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B.s_full[i], 1);
+      mbar_init(&B.p_ready[i][0], 4);
+      mbar_init(&B.p_ready[i][1], 4);
+      mbar_init(&B.pv_done[i], 1);
+    }
+    mbar_init(&B.done, 1);
+    B.abort = 0;
+    mbar_fence_init();
+    B.found_b = -1;
+  }
+  if (warp == 8 && lane < 3) tma_prefetch_map(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap);
   pdl_wait();
+  // tensor memory only now: a launch that held it while it waits could keep it from one that it waits for
 
   // ---- which rows: items count row-tile pairs from the last sequence's last pair (with a causal mask the largest)
   if (blockIdx.x == 0) check_sequences(a.kv, a.T, a.status);
-  if (threadIdx.x == 0) B.found_b = -1;
   __syncthreads();
   const int pair = 2 * w.tokens;
   for (int c0 = 0, base = 0; c0 < a.kv.n_seqs; c0 += kTcThreads) {
@@ -195,7 +224,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (item < base) break;
   }
   const int b = B.found_b;
-  if (b < 0) return;
+  if (b < 0) {
+    if (w.parts && split == 0 && threadIdx.x == 0) w.rows[unit] = make_int2(0, 0);
+    return;
+  }
   const SeqView s = seq_view(a.kv.q_start, a.kv.kv_len, b, a.kv.per, a.T, a.kv.cap);
   const int tok0 = B.found_t * pair;
   const int nq = s.m - tok0 > w.tokens ? 2 : 1;
@@ -203,30 +235,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int p0 = base + tok0, p1 = base + min(s.m, tok0 + pair) - 1;
   const TileRange tr = tile_range(p0, p1, s.n, a.window, a.n_sinks, kTcLogBK);
   // this CTA's key tiles: t0 .. t0 + nt - 1 of the range
-  const int tile0 = (int)((long long)tr.count * split >> w.log_splits);
-  const int nt = (int)((long long)tr.count * (split + 1) >> w.log_splits) - tile0;
+  int tile0, nt;
+  if (w.parts) {  // count x parts stays below 2^31: positions are below 2^30
+    tile0 = tr.count * split / w.parts;
+    nt = tr.count * (split + 1) / w.parts - tile0;
+    if (split == 0 && threadIdx.x == 0) w.rows[unit] = make_int2(s.q0 + tok0, min(s.m - tok0, pair));
+  } else {
+    tile0 = (int)((long long)tr.count * split >> w.log_splits);
+    nt = (int)((long long)tr.count * (split + 1) >> w.log_splits) - tile0;
+  }
   const int32_t *table = a.kv.table + (size_t)b * a.kv.max_pages;
 
-  if (threadIdx.x < 128) B.tok[threadIdx.x] = (uint8_t)min((int)threadIdx.x / a.G, w.tokens);
-  if (threadIdx.x == 0) {
-    mbar_init(&B.q_full, 1);
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&B.k_full[i], 1);
-      mbar_init(&B.k_empty[i], 1);
-      mbar_init(&B.v_full[i], 1);
-      mbar_init(&B.v_ready[i], 2);
-      mbar_init(&B.v_empty[i], 3);  // the products' commit and the two clearing warps
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&B.s_full[i], 1);
-      mbar_init(&B.p_ready[i][0], 4);
-      mbar_init(&B.p_ready[i][1], 4);
-      mbar_init(&B.pv_done[i], 1);
-    }
-    mbar_init(&B.done, 1);
-    B.abort = 0;
-    mbar_fence_init();
-  }
   if (warp == 9) tmem_alloc(&B.tmem, C::kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -391,9 +410,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
   }
-  if (splits > 1) {  // the meetings of the cluster's parts, below
+  if (splits > 1) {  // the meetings of the parts, below
     __syncthreads();
-    cluster_meet();
+    if (!w.parts) cluster_meet();
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -555,11 +574,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     if (splits > 1) {
       // ---- the cluster's parts: O of this CTA's keys into the stages' place, rows of D fp32 in swizzled 16-byte
-      // pieces.  CTA r mod splits finishes row r: it gets the others' (m, l) into its shared memory, and their rows by
-      // way of the workspace (L2 carries whole rows at once; fetched through distributed shared memory 64 KB took
-      // 7.5 us).
+      // pieces.  A CTA finishes every splits-th part of the rows: it gets the others' (m, l) into its shared memory, and their rows by
+      // way of the workspace in one asynchronous copy an owner (fetched through distributed shared memory 64 KB took
+      // 7.5 us, stored to the workspace by the threads 2.3 us).  Parts without a cluster go there whole.
       constexpr int kQuads = D / 4;
-      const int own = 256 >> w.log_splits;
+      const int log_own = 6 + nq - w.log_splits, own = 1 << log_own;  // rows a CTA finishes: nq * 128 / splits
       __syncthreads();  // no product or copy needs the stages any more
       if ((warp >> 2) < nq) {
         const int i = warp >> 2, row = threadIdx.x & 127, r = i * 128 + row;
@@ -583,23 +602,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<uint4 *>(os + ((((c + e) >> 2) ^ (row & (kQuads - 1))) << 2)) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
-        const int k = r >> w.log_splits, owner = r & (splits - 1);
-        cluster_store2(cluster_map(smem_u32(&B.ml[split * own + k]), owner), m, l);
+        if (w.parts) {
+          __stcg(w.ml + (size_t)blockIdx.x * 256 + r, make_float2(m, l));
+        } else {
+          const int owner = r >> log_own, k = r & (own - 1);
+          cluster_store2(cluster_map(smem_u32(&B.ml[(split << 8 >> w.log_splits) + k]), owner), m, l);
+        }
       }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       named_bar(1, 256);
       constexpr int kRowsOnce = 32 / kQuads;
       const int sub = lane % kQuads, first = warp * kRowsOnce + lane / kQuads;
-      float *parts = a.part + (size_t)(blockIdx.x - split) * 256 * D;  // of the cluster
+      float *parts = a.part + (size_t)(blockIdx.x - split) * 256 * D;  // of the item
       const float *mine = reinterpret_cast<const float *>(k_s);
-#pragma unroll 8
-      for (int r = first; r < nq * 128; r += 8 * kRowsOnce)
-        if ((r & (splits - 1)) != split)
-          __stcg(reinterpret_cast<float4 *>(parts + ((size_t)split * 256 + r) * D) + sub,
-                 *reinterpret_cast<const float4 *>(mine + (size_t)r * D + ((sub ^ (r & (kQuads - 1))) << 2)));
+      if (threadIdx.x < splits && (w.parts ? threadIdx.x == 0 && nt > 0 : (int)threadIdx.x != split)) {
+        const int rows = w.parts ? nq * 128 : own, r = w.parts ? 0 : (int)threadIdx.x * own;
+        bulk_store(parts + ((size_t)split * 256 + r) * D, smem_u32(mine + (size_t)r * D), (uint32_t)(rows * D * 4));
+      }
       __syncwarp();
-      cluster_meet();  // releases and acquires what went to the workspace too
+      if (!w.parts) cluster_meet();  // releases and acquires what went to the workspace too
       const TcRows where{a.out + ((size_t)s.q0 * a.H + (size_t)hv * a.G) * D, a.H, a.G, tok0, w.tokens, s.m, nq};
-      if (w.log_splits == 1)
+      if (w.parts)
+        ;  // attn_tc_join_kernel
+      else if (w.log_splits == 1)
         tc_join<D, 1>(where, B.ml, B.tok, mine, parts, split, first, sub);
       else if (w.log_splits == 2)
         tc_join<D, 2>(where, B.ml, B.tok, mine, parts, split, first, sub);
@@ -615,10 +640,132 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
+// The parts of one row, in order: 8 warps take every 8th part each (D = 64: two at a time), their sums are added in
+// order.  A part that saw nothing of the row has the weight 0, whatever lies in its place.
+template <int D>
+__global__ void __launch_bounds__(256) attn_tc_join_kernel(const __grid_constant__ TcArgs w) {
+  constexpr int kQuads = D / 4, kLanes = 256 / kQuads;
+  __shared__ float f_s[kAttnSms], warp_s[8];
+  __shared__ float4 o_s[kLanes][kQuads], v_s[10][256];
+  const AttnArgs &a = w.a;
+  const int unit = blockIdx.x >> 8, r = blockIdx.x & 255, hv = unit % a.V, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rr = r & 127, rt = rr / a.G, tk = (r >> 7) * w.tokens + rt;
+  pdl_release();
+  pdl_wait();
+  const int2 rows = __ldcg(w.rows + unit);
+  if (rt >= w.tokens || tk >= rows.y) return;
+  const int p = threadIdx.x;
+  const float2 x = p < w.parts ? __ldcg(w.ml + ((size_t)unit * w.parts + p) * 256 + r) : make_float2(-INFINITY, 0.f);
+  float mx = x.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (lane == 0) warp_s[warp] = mx;
+  __syncthreads();
+  mx = warp_s[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) mx = fmaxf(mx, warp_s[i]);
+  const float f = ex2(x.x - (mx == -INFINITY ? 0.f : mx));
+  if (p < w.parts) f_s[p] = f;
+  float sum = f * x.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  __syncthreads();
+  if (lane == 0) warp_s[warp] = sum;
+  const int q = threadIdx.x % kQuads, first = threadIdx.x / kQuads;
+  const float4 *o = reinterpret_cast<const float4 *>(a.part + ((size_t)unit * w.parts * 256 + r) * D) + (q ^ (r & (kQuads - 1)));
+  float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int k0 = first; k0 < w.parts; k0 += 10 * kLanes) {
+    // by way of shared memory: the compiler would wait for each load before it issues the next
+#pragma unroll
+    for (int i = 0; i < 10; ++i) cp_async16(&v_s[i][threadIdx.x], o + (size_t)min(k0 + i * kLanes, w.parts - 1) * 256 * kQuads);
+    cp_async_wait_all();
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+      const int k = k0 + i * kLanes;
+      const float g = k < w.parts ? f_s[k] : 0.f;
+      const float4 v = g == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : v_s[i][threadIdx.x];
+      y[0] += g * v.x;
+      y[1] += g * v.y;
+      y[2] += g * v.z;
+      y[3] += g * v.w;
+    }
+  }
+  o_s[first][q] = make_float4(y[0], y[1], y[2], y[3]);
+  __syncthreads();
+  if (threadIdx.x >= kQuads) return;
+  float total = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) total += warp_s[i];
+  float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kLanes; ++i) {
+    const float4 v = o_s[i][q];
+    z[0] += v.x;
+    z[1] += v.y;
+    z[2] += v.z;
+    z[3] += v.w;
+  }
+  const float inv = total == 0.f ? 0.f : 1.0f / total;
+  uint16_t *dst = a.out + ((size_t)(rows.x + tk) * a.H + (size_t)hv * a.G + rr - rt * a.G) * D + q * 4;
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(z[0] * inv, z[1] * inv), pack_bf16x2(z[2] * inv, z[3] * inv));
+}
+
+// The same with a warp a row, for up to 32 parts, of which a lane has 10 in flight (D = 64: two half warps take turns).
+// With 8 warps a row 16 items of 9 parts took 25 us, most of it waits of blocks that had one load each.
+template <int D>
+__global__ void __launch_bounds__(256) attn_tc_join_few_kernel(const __grid_constant__ TcArgs w) {
+  constexpr int kQuads = D / 4, kLanes = 32 / kQuads;
+  __shared__ float4 v_s[10][256];
+  const AttnArgs &a = w.a;
+  const int lane = threadIdx.x & 31, at = blockIdx.x * 8 + (threadIdx.x >> 5), unit = at >> 8, r = at & 255, hv = unit % a.V;
+  const int rr = r & 127, rt = rr / a.G, tk = (r >> 7) * w.tokens + rt;
+  pdl_release();
+  pdl_wait();
+  const int2 rows = __ldcg(w.rows + unit);
+  const float2 x = lane < w.parts ? __ldcg(w.ml + ((size_t)unit * w.parts + lane) * 256 + r) : make_float2(-INFINITY, 0.f);
+  if (rt >= w.tokens || tk >= rows.y) return;
+  float mx = x.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float f = ex2(x.x - (mx == -INFINITY ? 0.f : mx));
+  float sum = f * x.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const int q = lane % kQuads, first = lane / kQuads;
+  const float4 *o = reinterpret_cast<const float4 *>(a.part + ((size_t)unit * w.parts * 256 + r) * D) + (q ^ (r & (kQuads - 1)));
+  float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int k0 = 0; k0 < w.parts; k0 += 10 * kLanes) {
+#pragma unroll
+    for (int i = 0; i < 10; ++i)
+      cp_async16(&v_s[i][threadIdx.x], o + (size_t)min(k0 + i * kLanes + first, w.parts - 1) * 256 * kQuads);
+    cp_async_wait_all();
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+      const int k = k0 + i * kLanes + first;
+      const float fk = __shfl_sync(0xffffffffu, f, k & 31), g = k < w.parts ? fk : 0.f;
+      const float4 v = g == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : v_s[i][threadIdx.x];
+      y[0] += g * v.x;
+      y[1] += g * v.y;
+      y[2] += g * v.z;
+      y[3] += g * v.w;
+    }
+  }
+  if constexpr (kLanes == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] += __shfl_xor_sync(0xffffffffu, y[i], 16);
+    if (first) return;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+  uint16_t *dst = a.out + ((size_t)(rows.x + tk) * a.H + (size_t)hv * a.G + rr - rt * a.G) * D + q * 4;
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv));
+}
+
 template <int D>
 cudaError_t launch_tc(const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) {
   using C = TcCfg<D>;
-  TcArgs w{a, kTcRows / a.G, 0};
+  TcArgs w{a, kTcRows / a.G, 0, 0, nullptr, nullptr};
   auto fn = tma_encode_fn();
   if (!fn) return cudaErrorNotSupported;
   CUtensorMap qm, km, vm;
@@ -635,14 +782,34 @@ cudaError_t launch_tc(const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) 
   if (!make_pages_map(&km, c.k, c.n_pages, a, D, kTcBK) || !make_pages_map(&vm, c.v, c.n_pages, a, D, kTcBK))
     return cudaErrorInvalidValue;
   const int pair = 2 * w.tokens;
-  const long long items = a.kv.q_start ? (long long)a.T / pair + std::min(a.T, a.kv.n_seqs)
+  // m_1 + m_2 + ... = T of n sequences: the pairs of each, rounded up, are at most these
+  const long long items = a.kv.q_start ? (a.T + (long long)std::min(a.T, a.kv.n_seqs) * (pair - 1)) / pair
                                        : (long long)a.kv.n_seqs * ((a.kv.per + pair - 1) / pair);
   if (items * a.V > 0x7fffffffll) return cudaErrorInvalidValue;
+  // the key tiles of an item, at most
+  const long long span = a.window > 0 ? std::min<long long>(a.kv.cap, (long long)a.window + pair + a.n_sinks) : a.kv.cap;
+  const int tiles = (int)((span + kTcBK - 1) / kTcBK);
   // Clusters share the keys of an item where the items leave half of the SMs idle and the longest sequence gives every
-  // CTA two key tiles.
-  while (w.log_splits < 3 && (items * a.V << (w.log_splits + 1)) <= kAttnSms && a.kv.cap / kTcBK >= 4 << w.log_splits)
+  // CTA two key tiles.  Of 8 CTAs no more than 14 find room at once (16 items: two rounds, 86 us instead of 46).
+  const int units = (int)(items * a.V);
+  while (w.log_splits < 3 && (units << (w.log_splits + 1)) <= (w.log_splits == 2 ? 14 * 8 : kAttnSms) &&
+         tiles >= 4 << w.log_splits)
     ++w.log_splits;
-  const unsigned splits = 1u << w.log_splits;
+  // Parts without a cluster, joined by a second launch, may be any number: where that saves two steps of the longest
+  // item (2 us each; the launch and its loads take about 4), or costs none and small clusters would share few items.
+  // 16 tokens on 32768: 63 us with a cluster of 8, 18 so; 600 on 16000 141 and 104; 100 on 700 20.6 and 17.8; but 512
+  // on 1500 21.4 and 24.3, 1024 alone 21 and 27.
+  const int parts = units <= kAttnSms / 2 ? std::min(kAttnSms / units, tiles / 2) : 1;
+  if (parts > 1) {
+    const int with = (tiles + (1 << w.log_splits) - 1) >> w.log_splits, without = (tiles + parts - 1) / parts;
+    if (without + 2 <= with || (without <= with && w.log_splits < 3 && units <= 12)) {
+      w.parts = parts;
+      w.log_splits = 0;
+      w.ml = reinterpret_cast<float2 *>(a.part + (size_t)kAttnSms * 256 * D);
+      w.rows = reinterpret_cast<int2 *>(w.ml + kAttnSms * 256);
+    }
+  }
+  const unsigned splits = w.parts ? w.parts : 1u << w.log_splits;
   // the register shares have to be what the launch holds: raising them waits for what the others give up
   cudaFuncAttributes fa;
   cudaError_t err = cudaFuncGetAttributes(&fa, attn_tc_kernel<D>);
@@ -651,7 +818,11 @@ cudaError_t launch_tc(const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) 
   const size_t smem = (size_t)C::kSmemTiles * C::kTileBytes + sizeof(TcBars<D>) + 1024;
   err = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  return launch_dependent(attn_tc_kernel<D>, (unsigned)(items * a.V) * splits, kTcThreads, smem, splits, s, qm, km, vm, w);
+  err = launch_dependent(attn_tc_kernel<D>, (unsigned)(items * a.V) * splits, kTcThreads, smem, w.parts ? 1 : splits, s, qm,
+                         km, vm, w);
+  if (err != cudaSuccess || !w.parts) return err;
+  if (w.parts <= 32) return launch_dependent(attn_tc_join_few_kernel<D>, (unsigned)units * 32, 256, 0, 1, s, w);
+  return launch_dependent(attn_tc_join_kernel<D>, (unsigned)units * 256, 256, 0, 1, s, w);
 }
 
 }  // namespace

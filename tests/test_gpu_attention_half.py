@@ -257,6 +257,11 @@ CHUNKS = [  # H, V, D, page, new, totals, window, sinks
     (16, 2, 128, 64, [16], [9000], 0, 0),
     (8, 2, 64, 16, [200], [5000], 0, 0),
     (20, 1, 128, 32, [11, 40], [4000, 60], 0, 0),
+    (8, 1, 128, 64, [16], [40000], 0, 0),                     # few rows over long caches: parts joined by a second launch
+    (6, 2, 64, 32, [30, 1], [9000, 3], 0, 0),
+    (7, 1, 128, 16, [20, 0, 13], [13, 0, 17000], 6000, 3),
+    (128, 1, 64, 64, [3], [30000], 0, 0),
+    (4, 4, 64, 16, [40], [5000], 5000, 0),
     (6, 1, 64, 128, [12, 9, 30], [12, 3000, 900], 700, 9),
     (4, 1, 64, 16, [i % 11 for i in range(700)], [i % 11 + i % 70 for i in range(700)], 0, 0),
 ]
