@@ -7,7 +7,7 @@
 // in base 2 with scale * log2(e) folded in.  Both products have the keys or the head dimension on the 16-row side and
 // the query rows on the 8-column side (S^T = K Q^T, O^T = V^T P^T).
 //
-// Split: all key tiles of all (sequence, key/value head, row tile) groups stand in one line, which is cut into equal
+// Split: all key tiles of all (sequence, key/value head) groups stand in one line, which is cut into equal
 // shares, one a CTA, whatever the lengths (they are read on the device, so that a captured graph follows them).
 // (Smaller shares taken as CTAs come free were slower: every share's ends cost more than the balance gave.)  A group
 // that is cut leaves parts (m, l, o) in the workspace; the CTA that brings the last one joins them in share order, so
@@ -37,10 +37,13 @@ namespace {
 
 constexpr float kWinLazy = 8.0f;
 constexpr int kJoinParts = 12;  // more parts a group go to the second launch (4: 7 sequences 36 us instead of 25)
-// Windows of more rows go to the chunk kernel's tiles where they fill the SMs: 32 x 8 tokens of 8 heads a group at 8192
-// 66 us there, 131 here; 32 x 3 tokens 65 and 73, but 64 ragged sequences 216 and 135, as a chunk tile walks a whole
-// sequence, and so up to 32 rows stay.
-constexpr int kTcMinRows = 32;
+// Windows of more than 32 rows go to the chunk kernel's tiles (32 x 8 tokens of 8 heads a group at 8192: 66 us there,
+// 131 here when this kernel still walked the keys once for 32 rows each), and those of 17 to 32 where it has five parts
+// or more for each sequence and key/value head (8 x 3 tokens at 16000: 36 us there, 46 here; 8 and 12 ragged up to 4000
+// 17 and 20, 25 and 23).  More sequences stay, as few or no parts cannot even out their lengths (64 x 3 ragged up to
+// 16384: 214 there, 135 here; but 64 x 3 at 1024 all 21 and 29), and so do 16 rows or fewer (8 x 2 ragged up to 16384:
+// 32 there, 21 here).
+constexpr int kWinRows = 32, kWinFew = kAttnSms / 5;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -92,7 +95,7 @@ constexpr int kRecEnd = 8;                   // no tile: the CTA is done
 
 // What the producer tells beside a stage.
 struct TileRec {
-  int b, hv, rt;      // the group: sequence, key/value head, row tile
+  int b, hv;          // the group: sequence, key/value head
   int j0, n;          // first key of the tile, keys of the sequence
   int q;              // with `first`: which of the places holds the group's queries
   int flags;          // kRec...
@@ -110,7 +113,6 @@ struct WinBars {
 
 struct WinArgs {
   AttnArgs a;
-  int row_tiles;
   int join_after;  // parts are joined by attn_join_kernel
 };
 
@@ -181,12 +183,12 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
   __shared__ long long sum_s[C::kThreads / 32];
   __shared__ __align__(16) float row_s[C::kRows][4];  // maxima, or sums, of each row by warp
   __shared__ __align__(16) uint16_t use_s[2][8];  // by turns: a warp may be one tile ahead
-  __shared__ uint8_t tok_s[NR == 4 ? 1024 : C::kRows];  // the token of each row
+  __shared__ uint8_t tok_s[C::kRows];  // the token of each row
   __shared__ __align__(4) uint16_t mask_s[C::kWarps][8 * C::kNR];  // keys of a warp's 16 that each row sees
   __shared__ int last_s;
   const AttnArgs &a = w.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int groups = a.V * w.row_tiles, rows = a.kv.per * a.G;
+  const int groups = a.V, rows = a.kv.per * a.G;
   const uint32_t smem0 = smem_u32(win_smem);
   pdl_release();
   if (threadIdx.x == 0) {
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
     mbar_fence_init();
   }
 
-  for (int i = threadIdx.x; i < w.row_tiles * C::kRows; i += C::kThreads) tok_s[i] = (uint8_t)min(i / a.G, 255);
+  for (int i = threadIdx.x; i < C::kRows; i += C::kThreads) tok_s[i] = (uint8_t)min(i / a.G, 255);
 
   pdl_wait();
 
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
     TileRange r = window_tiles(a, s, C::kLogBK);
     const int gi = x1 > x0 ? (int)mul_div(x0 - line, 1, r.count) : 0;
     int t = x1 > x0 ? (int)(x0 - line - (long long)gi * r.count) : 0;
-    int hv = gi / w.row_tiles, rt = gi - hv * w.row_tiles;
+    int hv = gi;
     // this lane's piece of the tile at the cursor
     auto piece = [&](bool &seen) {
       const int a0 = (tile_of(r, t) << C::kLogBK) + (lane << log_pc), e0 = a0 + pc;
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
       const bool ok = seen && page >= 0 && page < a.kv.n_pages;
       const uint32_t good = __ballot_sync(0xffffffffu, ok), wrong = __ballot_sync(0xffffffffu, seen && !ok);
       const bool first = x == x0 || t == 0;
-      const int j0 = tile_of(r, t) << C::kLogBK, cb = b, chv = hv, crt = rt;
+      const int j0 = tile_of(r, t) << C::kLogBK, cb = b, chv = hv;
       // below 2^31: checked on the host
       const int row = ((page * a.V + hv) << a.kv.log_ps) + ((j0 + (lane << log_pc)) & ((1 << a.kv.log_ps) - 1));
       if (lane == 0) {
@@ -269,7 +271,6 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
         const bool last = x + 1 == x1 || t + 1 == r.count;
         rec.b = b;
         rec.hv = hv;
-        rec.rt = rt;
         rec.j0 = j0;
         rec.n = s.n;
         rec.q = qn;
@@ -313,15 +314,12 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
       // the cursor, and the next tile's pages, which come in while this warp waits for a stage
       if (++t == r.count) {
         t = 0;
-        if (++rt == w.row_tiles) {
-          rt = 0;
-          if (++hv == a.V) {
-            hv = 0;
-            if (b + 1 == a.kv.n_seqs) x1 = x + 1;
-            if (x + 1 < x1) {
-              s = seq_view(nullptr, a.kv.kv_len, ++b, a.kv.per, a.T, a.kv.cap);
-              r = window_tiles(a, s, C::kLogBK);
-            }
+        if (++hv == a.V) {
+          hv = 0;
+          if (b + 1 == a.kv.n_seqs) x1 = x + 1;
+          if (x + 1 < x1) {
+            s = seq_view(nullptr, a.kv.kv_len, ++b, a.kv.per, a.T, a.kv.cap);
+            r = window_tiles(a, s, C::kLogBK);
           }
         }
       }
@@ -332,9 +330,9 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
         const uint32_t dst = smem0 + C::kQAt + (uint32_t)qn * C::kQBytes;
         qn = qn + 1 == C::kStages ? 0 : qn + 1;
         for (int i = lane; i < C::kRows * kChunks; i += 32) {
-          const int rr = i / kChunks, ch = i % kChunks, rg = crt * C::kRows + rr, tok = tok_s[rg];
-          const bool in = rg < rows;
-          const uint16_t *src = a.q + (in ? (size_t)(cb * a.kv.per + tok) * a.ld_q + (size_t)(chv * a.G + rg - tok * a.G) * D + ch * 8 : 0);
+          const int rr = i / kChunks, ch = i % kChunks, tok = tok_s[rr];
+          const bool in = rr < rows;
+          const uint16_t *src = a.q + (in ? (size_t)(cb * a.kv.per + tok) * a.ld_q + (size_t)(chv * a.G + rr - tok * a.G) * D + ch * 8 : 0);
           cp_async16_or_zero(dst + (uint32_t)(rr * kChunks + (ch ^ (rr & 7))) * 16u, src, in);
         }
       }
@@ -424,7 +422,7 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
         // which of the warp's keys some row sees, and of these the ones whose values are not finite: 0 * v is NaN
         // then, so that where rows differ in what they see such a key is left out of the product, and the rows that
         // see it become NaN
-        const int n = rec.n, j0 = rec.j0, base_pos = n - a.kv.per, r0 = rec.rt * C::kRows + rb;
+        const int n = rec.n, j0 = rec.j0, base_pos = n - a.kv.per;
 #pragma unroll
         for (int t = 0; t < C::kMK; ++t) {
           // lane and lane + 16 look at one key, half of its values each
@@ -446,7 +444,7 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
           if (lane == 0 && warp < 4) use_s[turn][C::kMK * wq + t] = (uint16_t)(lv & ~bd);
 #pragma unroll
           for (int r = lane; r < 8 * C::kNR; r += 32) {
-            const int hi = r0 + r < rows ? base_pos + tok_s[r0 + r] - (j0 + k0) : -1;  // keys up to hi,
+            const int hi = rb + r < rows ? base_pos + tok_s[rb + r] - (j0 + k0) : -1;  // keys up to hi,
             const int lo = a.window > 0 ? hi - a.window + 1 : 0;                       // from lo on
             const int sk = a.window > 0 ? a.n_sinks - (j0 + k0) : 0;                   // or below sk
             mask_s[warp][r] = (uint16_t)(below(hi + 1) & (~below(lo) | below(sk)) & lv);
@@ -578,7 +576,7 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
       }
     }
     turn ^= 1;
-    int c0 = 0, c1 = 0, slot = 0, slot0 = 0, hv = 0, q0 = 0, r0 = 0;
+    int c0 = 0, c1 = 0, slot = 0, slot0 = 0, hv = 0, q0 = 0;
     if (flags & kRecLast) {
       c0 = rec.c0;
       c1 = rec.c1;
@@ -586,7 +584,6 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
       slot0 = rec.slot0;
       hv = rec.hv;
       q0 = rec.b * a.kv.per;
-      r0 = rec.rt * C::kRows;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&B.empty[cs]);
@@ -607,7 +604,7 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
         if (g == 0) row_s[rb + 8 * i + 2 * c + e][wq] = x;
       }
     win_meet(false, kMeet);
-    const int live = min(rows - r0, C::kRows);
+    const int live = rows;
     constexpr size_t kPart = (size_t)C::kRows * (D + 2);
     float *po = a.part + ((size_t)share * 2 + slot) * kPart, *pm = po + (size_t)C::kRows * D;
 #pragma unroll
@@ -620,8 +617,8 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
         const float sum = (x.x + x.y) + (x.z + x.w);
         if (c0 == c1) {
           const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-          const int rg = r0 + r, tok = tok_s[rg];
-          uint16_t *dst = a.out + ((size_t)(q0 + tok) * a.H + (size_t)hv * a.G + rg - tok * a.G) * D + col;
+          const int tok = tok_s[r];
+          uint16_t *dst = a.out + ((size_t)(q0 + tok) * a.H + (size_t)hv * a.G + r - tok * a.G) * D + col;
 #pragma unroll
           for (int t = 0; t < C::kMD; ++t) {
             dst[16 * t] = float_to_bf16_bits(o[t][i][e] * inv);
@@ -693,7 +690,7 @@ __global__ void __launch_bounds__(WinCfg<D, NR>::kThreads, WinCfg<D, NR>::kCtas)
         const int i = i0 + u * kMeet;
         if (i >= live * (D / 4)) continue;
         const float inv = ll[u] == 0.f ? 0.f : 1.0f / ll[u];
-        const int rg = r0 + i / (D / 4), tok = tok_s[rg];
+        const int rg = i / (D / 4), tok = tok_s[rg];
         uint16_t *dst = a.out + ((size_t)(q0 + tok) * a.H + (size_t)hv * a.G + rg - tok * a.G) * D + 4 * (i % (D / 4));
         *reinterpret_cast<uint2 *>(dst) =
             make_uint2(pack_bf16x2(y[u][0] * inv, y[u][1] * inv), pack_bf16x2(y[u][2] * inv, y[u][3] * inv));
@@ -711,12 +708,11 @@ __global__ void __launch_bounds__(512) attn_join_kernel(const __grid_constant__ 
   __shared__ float4 o_s[kLanes][kQuads];
   __shared__ long long total_s[17];
   const AttnArgs &a = w.a;
-  const int groups = a.V * w.row_tiles, rows = a.kv.per * a.G;
-  const int r = blockIdx.x % tile_rows, group = blockIdx.x / tile_rows % groups, b = blockIdx.x / tile_rows / groups;
-  const int hv = group / w.row_tiles, rg = (group - hv * w.row_tiles) * tile_rows + r;
+  const int groups = a.V, rows = a.kv.per * a.G;
+  const int r = blockIdx.x % tile_rows, hv = blockIdx.x / tile_rows % groups, b = blockIdx.x / tile_rows / groups;
   pdl_release();
   pdl_wait();
-  if (rg >= rows) return;
+  if (r >= rows) return;
   // the line, and where this sequence stands in it
   long long total = 0, line = 0;
   for (int i = threadIdx.x; i < a.kv.n_seqs; i += 512) {
@@ -743,7 +739,7 @@ __global__ void __launch_bounds__(512) attn_join_kernel(const __grid_constant__ 
   }
   total *= groups;
   const int count = window_count(a, b, log_bk), shares = (int)min((long long)ctas, total);
-  const long long gs = line * groups + (long long)group * count, ge = gs + count;
+  const long long gs = line * groups + (long long)hv * count, ge = gs + count;
   const int c0 = share_of(gs, shares, total), c1 = share_of(ge - 1, shares, total);
   if (c0 == c1) return;  // not cut
   const int slot0 = gs > mul_div(total, c0, shares);
@@ -799,8 +795,8 @@ __global__ void __launch_bounds__(512) attn_join_kernel(const __grid_constant__ 
     z[3] += v.w * f;
   }
   const float inv = ll == 0.f ? 0.f : 1.0f / ll;
-  const int tok = rg / a.G;
-  uint16_t *dst = a.out + ((size_t)(b * a.kv.per + tok) * a.H + (size_t)hv * a.G + rg - tok * a.G) * D + 4 * q;
+  const int tok = r / a.G;
+  uint16_t *dst = a.out + ((size_t)(b * a.kv.per + tok) * a.H + (size_t)hv * a.G + r - tok * a.G) * D + 4 * q;
   *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(z[0] * inv, z[1] * inv), pack_bf16x2(z[2] * inv, z[3] * inv));
 }
 
@@ -810,12 +806,11 @@ cudaError_t launch(WinArgs w, const moe_kv_cache &c, cudaStream_t s) {
   CUtensorMap km, vm;
   if (!make_pages_map(&km, c.k, c.n_pages, w.a, D, C::kBK) || !make_pages_map(&vm, c.v, c.n_pages, w.a, D, C::kBK))
     return cudaErrorInvalidValue;
-  w.row_tiles = (w.a.kv.per * w.a.G + C::kRows - 1) / C::kRows;
   cudaError_t err = cudaFuncSetAttribute(attn_window_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (err != cudaSuccess) return err;
   // more than kJoinParts parts a group, were all sequences alike: the second launch
   const int ctas = kAttnSms * C::kCtas;
-  const long long groups = (long long)w.a.kv.n_seqs * w.a.V * w.row_tiles;
+  const long long groups = (long long)w.a.kv.n_seqs * w.a.V;
   w.join_after = groups * kJoinParts < ctas && w.a.kv.cap > kJoinParts * C::kBK;
   err = launch_dependent(attn_window_kernel<D, NR>, ctas, C::kThreads, C::kSmem, 1, s, km, vm, w);
   if (err == cudaSuccess && w.join_after)
@@ -823,7 +818,7 @@ cudaError_t launch(WinArgs w, const moe_kv_cache &c, cudaStream_t s) {
   return err;
 }
 
-// Rows of a window: one, two or four 8-row tiles side by side; more rows than 32 walk the keys again.
+// Rows of a window: one, two or four 8-row tiles side by side.
 template <int D>
 cudaError_t launch_d(const WinArgs &w, const moe_kv_cache &c, cudaStream_t s) {
   const int rows = w.a.kv.per * w.a.G;
@@ -854,11 +849,11 @@ size_t attn_part_bytes(const moe_attn_dims &d, int, int) {
 }
 
 cudaError_t launch_attn(const moe_attn_dims &d, const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) {
-  WinArgs w{a, 1, 0};
+  const WinArgs w{a, 0};
   trace_mark(MOE_KERNEL_ATTN, false, s);
   const int rows = a.kv.per * a.G;
-  const bool fills = (long long)a.kv.n_seqs * a.V * 8 >= kAttnSms / 2;  // with clusters of 8
-  const bool window = !a.kv.q_start && a.kv.per <= 8 && !(rows > kTcMinRows && fills);
+  const bool few = rows > 16 && (long long)a.kv.n_seqs * a.V <= kWinFew;
+  const bool window = !a.kv.q_start && a.kv.per <= 8 && rows <= kWinRows && !few;
   const cudaError_t err = !window             ? launch_attn_tc(d, a, c, s)
                           : d.head_dim == 128 ? launch_d<128>(w, c, s)
                                               : launch_d<64>(w, c, s);

@@ -339,7 +339,8 @@ typedef struct {
  * A sequence with kv_len[b] = 0 is padding: its rows stand at negative positions.
  * Rows of no sequence (before q_start[0], at or after q_start[n_seqs]) are left as they
  * were.  What the device finds wrong sets MOE_ERR_DEVICE in the workspace status: a
- * q_start pair that decreases or leaves [0, T] makes that sequence empty, a kv_len
+ * q_start pair that decreases or leaves [0, T] makes that sequence empty (rows that two
+ * others then share may be left unwritten), a kv_len
  * outside [0, max_pages * page_size] counts as 0, and a token whose page is outside
  * [0, n_pages) is neither written nor seen. */
 typedef struct {
@@ -391,8 +392,8 @@ moe_status moe_qk_norm_rope(const moe_attn_dims *dims, const uint16_t *qkv, int6
  * window = 0: all earlier tokens; n_sinks >= 0 (without a window it changes nothing).
  * Which kernel runs: q_start == NULL and T <= 8 n_seqs (verify windows) splits the
  * cached lengths evenly over the SMs and joins the parts; anything else (prompt
- * chunks), and windows of more than 32 rows (new tokens x group) where these fill
- * the SMs, takes tiles of queries. */
+ * chunks), windows of more than 32 rows (new tokens x group) and of more than 16 with
+ * n_seqs * n_kv_heads <= 29 takes tiles of queries. */
 moe_status moe_attn_forward(const moe_attn_dims *dims, const uint16_t *q, int64_t ld_q, const moe_kv_cache *cache,
                             const moe_kv_batch *batch, int32_t T, float scale, int32_t window, int32_t n_sinks,
                             uint16_t *out, void *workspace, size_t ws_bytes, moe_stream_t stream);

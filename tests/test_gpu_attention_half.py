@@ -230,6 +230,11 @@ WINDOWS = [  # H, V, D, page, new, totals, window, sinks
     (16, 2, 128, 64, 3, [70000], 0, 0),                       # many parts of few groups
     (80, 2, 128, 64, 5, [6000], 0, 0),
     (4, 2, 64, 16, 1, [1 + 7 * i % 90 for i in range(900)], 0, 0),
+    (8, 1, 128, 64, 3, [37 * i % 700 for i in range(40)], 0, 0),   # 17 to 32 rows of many groups
+    (20, 4, 64, 16, 4, [2900, 4, 0, 3, 100, 64, 65, 800, 15], 90, 5),
+    (32, 8, 64, 128, 6, [500, 129, 6, 3000], 0, 0),
+    (17, 1, 128, 32, 1, [5 * i for i in range(31)], 0, 0),
+    (16, 1, 128, 16, 2, [900 - 30 * i for i in range(30)], 333, 1),
 ]
 
 
@@ -368,6 +373,60 @@ def test_attention_pages_outside_the_cache(M, new):
             w = torch.softmax(s.masked_fill(~(keep & (j <= i)), -math.inf), -1)
             d = (out[new:, h].double() - w @ v[h // 2]).abs()
             assert (d <= 3 * H16 * (w @ v[h // 2].abs()) + 1e-6).all()
+
+
+PATHS = [  # H, V, D, page, new, totals
+    (4, 2, 64, 16, 20, [6000]),                              # some parts an item
+    (4, 1, 128, 64, 12, [20000]),                            # many
+    (8, 2, 64, 16, 6, [50 + 40 * i for i in range(16)]),     # a window of 24 rows, 32 groups
+    (16, 2, 128, 64, 3, [700] * 16),
+    (16, 2, 128, 32, 2, [9000]),                             # a window of 16 rows, many parts
+]
+
+
+@pytest.mark.parametrize("H,V,D,ps,new,total", PATHS)
+def test_attention_odd_inputs_on_every_path(M, H, V, D, ps, new, total):
+    """Scales of either sign and none, scores of thousands, values that are not finite, a bad page, padding."""
+    g = gen(31 + H + D)
+    n = len(total)
+    B = Batch(M, g, H, V, D, ps, [new] * n, total, fill=math.nan)
+    q = normal(g, B.T, H, D).bfloat16()
+    for scale in (1.0, -0.1, 0.0):
+        check_attention(M, B, q, scale=scale)
+    check_attention(M, B, (300 * q.float()).bfloat16())
+    # the last token of the last sequence: only its last query sees it
+    p = total[-1] - 1
+    pg, r = int(B.table[n - 1, p // ps]), p % ps
+    kept = B.v[pg, 0, r].clone()
+    out = torch.empty((B.T, H, D), device="cuda", dtype=torch.bfloat16)
+    run = lambda: M.moe_attn_forward(B.dims, q, out, B.k, B.v, B.kv_len, B.table, B.ws, q_start=B.q_start)  # noqa: E731
+    run()
+    want = out.clone()
+    for bad in (math.inf, math.nan):
+        B.v[pg, 0, r] = bad
+        run()
+        M.moe_check_status(B.ws)
+        assert torch.equal(out[:-1], want[:-1]) and torch.equal(out[-1, H // V:], want[-1, H // V:])
+        assert not torch.isfinite(out[-1, :H // V]).any()
+    B.v[pg, 0, r] = kept
+    # a page outside the cache: its tokens are seen by nobody, and the next call is right again
+    at = (total[-1] - new - 1) // ps
+    page = int(B.table[n - 1, at])
+    B.table[n - 1, at] = -7
+    run()
+    with pytest.raises(M.MoeError) as e:
+        M.moe_check_status(B.ws)
+    assert e.value.code == 6
+    assert torch.equal(out[:-new], want[:-new]) and torch.isfinite(out).all()
+    B.table[n - 1, at] = page
+    # a sequence that is padding now
+    B.kv_len[0] = 0
+    run()
+    M.moe_check_status(B.ws)
+    assert (out[:new] == 0).all()
+    B.kv_len[0] = total[0]
+    run()
+    assert torch.equal(out, want)
 
 
 def test_attention_bad_sequences(M):
