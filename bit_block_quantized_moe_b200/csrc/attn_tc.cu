@@ -10,7 +10,8 @@
 // next Q K (700 and 620) paces it: 8192 tokens of 16 heads over 2 key/value heads take 252 us, 1095 TFLOP/s, with the
 // tensor core busy two thirds of the time.  Slower: two threads a row (309 us, the exchange of the halves' maxima), a
 // quarter or half of the exponentials as polynomials on the FMA units (264, 302: the special function unit is not the
-// limit), weights begun before the maximum is known (262).  m is the maximum seen so far, left as it is
+// limit), weights begun before the maximum is known (262), steps of 64 keys with two places for S, so that the next Q K
+// runs under the softmax (394: 64 columns take the tensor core as long as 128).  m is the maximum seen so far, left as it is
 // until a row exceeds it by 8 (a factor of 256, which fp32 sums and bf16 weights carry without loss: only then are l
 // and O_i, which lie in tensor memory, rescaled), so that the rescaling is rare.
 //   warps 0-3, 4-7 : softmax of row tile 0, 1, then its output rows;
@@ -19,7 +20,9 @@
 //   warps 10, 11   : V rows that must not be multiplied (keys that no row sees, non-finite values behind a mask)
 //                    are cleared before P V, in tiles with a mask only.
 // Few row tiles over many keys leave SMs idle: then a cluster of 2, 4 or 8 CTAs shares the key tiles of one pair of row
-// tiles.  Each finishes its part of the rows from all of their (m, l, O), in rank order.
+// tiles.  Each finishes its part of the rows from all of their (m, l, O), in rank order.  Where clusters, which are powers
+// of two and find no room beyond 14 of 8, would leave too many idle, parts in any number are joined by a second launch.
+// 1024 tokens alone take 21 us (2 CTAs a pair), 16 tokens on 32768 19 us (74 parts a key/value head).
 // Every wait on memory is bounded (sync.cuh).
 #include <algorithm>
 
@@ -810,7 +813,8 @@ cudaError_t launch_tc(const AttnArgs &a, const moe_kv_cache &c, cudaStream_t s) 
     }
   }
   const unsigned splits = w.parts ? w.parts : 1u << w.log_splits;
-  // the register shares have to be what the launch holds: raising them waits for what the others give up
+  // the register shares have to be what the launch holds: raising them waits for what the others give up (and all
+  // registers of an SM, so that no CTA of another launch holds tensor memory beside this one's)
   cudaFuncAttributes fa;
   cudaError_t err = cudaFuncGetAttributes(&fa, attn_tc_kernel<D>);
   if (err != cudaSuccess) return err;

@@ -48,6 +48,7 @@ struct LnCfg {
   static constexpr int kSumAt = kStages * kStageBytes;
   static constexpr int kBarsAt = kSumAt + kSumBytes;
   static_assert(kStageBytes % 1024 == 0, "stages keep the 1024-byte alignment of the 128-byte swizzle");
+  static_assert(kBarsAt >= (BN == 16 ? 72 : BN == 64 ? 144 : 192) * 1024, "what may share an SM: see tmem_alloc below");
 };
 
 template <int STAGES>
@@ -348,6 +349,9 @@ __global__ void __launch_bounds__(LnCfg<BN, SPLIT>::kThreads, 1)
     B.abort = 0;
     mbar_fence_init();
   }
+  // Tensor memory is taken before the wait (0.3 us earlier), although an earlier launch of the stream may have CTAs on
+  // this SM that have yet to take theirs: shared memory lets at most tiles of 64 and 16, or 16 and 16, columns stand
+  // together, 160 of 512 columns, and beside a CTA of attention's chunk kernel, which has all registers, nothing stands.
   if (warp == 0) tmem_alloc(&B.tmem, C::kTmemCols);
   tc_fence_before();
   if constexpr (SPLIT) cluster_meet();  // every CTA of the cluster is there before its memory is written
