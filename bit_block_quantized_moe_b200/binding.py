@@ -152,10 +152,10 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is None:
         # the handle itself: torch.cuda.current_stream() builds an object around it, 5 us against 0.3
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -280,15 +280,16 @@ _I32, _F32 = torch.int32, torch.float32
 
 
 def _check_tensors(what, half, others):
-    """Every tensor on the current CUDA device (the call launches there); `half` in bf16, or its bit patterns in
-    16-bit integers."""
-    dev = torch.cuda.current_device()
+    """Every tensor on the current CUDA device (the call launches there), which is returned; `half` in bf16, or its bit
+    patterns in 16-bit integers."""
+    dev = torch._C._cuda_getDevice()  # torch.cuda.current_device() asks for the initialisation too, 0.2 us
     for t in half:
         if t.get_device() != dev or t.dtype not in _BF16:
             raise ValueError(f"{what}: activations, weights and caches are bf16, on the current CUDA device")
     for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{what}: every tensor belongs on the current CUDA device")
+    return dev
 
 
 def moe_linear_workspace_bytes(max_T: int, K: int, N: int) -> int:
@@ -298,7 +299,7 @@ def moe_linear_workspace_bytes(max_T: int, K: int, N: int) -> int:
 def moe_linear(x, w, out, workspace, bias=None, act="none", resid=None, stream=None):
     """out = act(x w^T + bias) in bf16, or resid + that in fp32 (out may be resid).  x [T, K] bf16 (rows may be
     strided), w [N, K] bf16, bias [N] fp32, resid and out [T, N]."""
-    _check_tensors("moe_linear", (x, w), (out, workspace, bias, resid))
+    dev = _check_tensors("moe_linear", (x, w), (out, workspace, bias, resid))
     T, K = x.shape
     N = w.shape[0]
     if w.shape[1] != K or out.shape != (T, N) or (bias is not None and (bias.numel() != N or bias.dtype != _F32)) or (
@@ -311,7 +312,7 @@ def moe_linear(x, w, out, workspace, bias=None, act="none", resid=None, stream=N
         raise ValueError("moe_linear: only the rows of x may be strided")
     code = lib().moe_linear(x.data_ptr(), x.stride(0) if T > 1 else K, w.data_ptr(), _ptr(bias), MOE_ACT[act],
                             _ptr(resid), out.data_ptr(), T, K, N, workspace.data_ptr(), workspace.nbytes,
-                            _stream(stream))
+                            _stream(stream, dev))
     _check(code, "moe_linear")
 
 
@@ -327,8 +328,8 @@ def moe_attn_workspace_bytes(dims: moe_attn_dims, n_seqs: int, max_T: int) -> in
 
 def _cache_and_batch(what, dims, k_cache, v_cache, kv_len, page_table, q_start):
     shape = k_cache.shape
-    if len(shape) != 4 or shape[1] != dims.n_kv_heads or shape[2] != dims.page_size or shape[3] != dims.head_dim or (
-            v_cache.shape != shape) or not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+    if shape[1:] != (dims.n_kv_heads, dims.page_size, dims.head_dim) or v_cache.shape != shape or not (
+            k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError(f"{what}: k and v are contiguous [n_pages, n_kv_heads, page_size, head_dim]")
     n, pages = page_table.shape
     if kv_len.numel() != n or page_table.dtype != _I32 or kv_len.dtype != _I32 or not (
@@ -357,7 +358,7 @@ def moe_qk_norm_rope(dims, qkv, q_out, k_cache, v_cache, kv_len, page_table, wor
     """Per-head norms and rotation of qkv [T, (n_heads + 2 n_kv_heads) * head_dim]; queries to q_out [T, n_heads,
     head_dim], keys and values to their pages."""
     what = "moe_qk_norm_rope"
-    _check_tensors(what, (qkv, q_out, k_cache, v_cache), (kv_len, page_table, workspace, q_start, q_gain, k_gain))
+    dev = _check_tensors(what, (qkv, q_out, k_cache, v_cache), (kv_len, page_table, workspace, q_start, q_gain, k_gain))
     cache, batch = _cache_and_batch(what, dims, k_cache, v_cache, kv_len, page_table, q_start)
     ld = _token_rows("moe_qk_norm_rope: qkv", qkv, dims.n_heads + 2 * dims.n_kv_heads, dims.head_dim)
     T = qkv.shape[0]
@@ -370,7 +371,7 @@ def moe_qk_norm_rope(dims, qkv, q_out, k_cache, v_cache, kv_len, page_table, wor
     code = lib().moe_qk_norm_rope(ctypes.byref(dims), qkv.data_ptr(), ld, _ptr(q_gain), _ptr(k_gain), eps,
                                   None if rope is None else ctypes.byref(rope), ctypes.byref(cache),
                                   ctypes.byref(batch), T, q_out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-                                  _stream(stream))
+                                  _stream(stream, dev))
     _check(code, what)
 
 
@@ -379,7 +380,7 @@ def moe_attn_forward(dims, q, out, k_cache, v_cache, kv_len, page_table, workspa
     """Attention of q [T, n_heads, head_dim] (tokens may be strided) over the paged cache; scale defaults to
     head_dim ** -0.5."""
     what = "moe_attn_forward"
-    _check_tensors(what, (q, out, k_cache, v_cache), (kv_len, page_table, workspace, q_start))
+    dev = _check_tensors(what, (q, out, k_cache, v_cache), (kv_len, page_table, workspace, q_start))
     cache, batch = _cache_and_batch(what, dims, k_cache, v_cache, kv_len, page_table, q_start)
     ld = _token_rows("moe_attn_forward: q", q, dims.n_heads, dims.head_dim)
     T = q.shape[0]
@@ -387,7 +388,7 @@ def moe_attn_forward(dims, q, out, k_cache, v_cache, kv_len, page_table, workspa
         raise ValueError("moe_attn_forward: out is contiguous [T, n_heads, head_dim]")
     code = lib().moe_attn_forward(ctypes.byref(dims), q.data_ptr(), ld, ctypes.byref(cache), ctypes.byref(batch), T,
                                   dims.head_dim ** -0.5 if scale is None else scale, window, n_sinks, out.data_ptr(),
-                                  workspace.data_ptr(), workspace.nbytes, _stream(stream))
+                                  workspace.data_ptr(), workspace.nbytes, _stream(stream, dev))
     _check(code, what)
 
 
