@@ -201,38 +201,46 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (blockIdx.x == 0) check_sequences(a.kv, a.T, a.status);
   __syncthreads();
   const int pair = 2 * w.tokens;
-  for (int c0 = 0, base = 0; c0 < a.kv.n_seqs; c0 += kTcThreads) {
-    const int b = a.kv.n_seqs - 1 - (c0 + (int)threadIdx.x);
-    const int cnt = b >= 0 ? (seq_view(a.kv.q_start, a.kv.kv_len, b, a.kv.per, a.T, a.kv.cap).m + pair - 1) / pair : 0;
-    int incl = cnt;
+  int b, ft;
+  if (!a.kv.q_start) {
+    const int pairs = (a.kv.per + pair - 1) / pair, back = item / pairs;
+    b = a.kv.n_seqs - 1 - back;
+    ft = pairs - 1 - (item - back * pairs);
+  } else {
+    for (int c0 = 0, base = 0; c0 < a.kv.n_seqs; c0 += kTcThreads) {
+      const int b = a.kv.n_seqs - 1 - (c0 + (int)threadIdx.x);
+      const int cnt = b >= 0 ? (seq_view(a.kv.q_start, a.kv.kv_len, b, 0, a.T, a.kv.cap).m + pair - 1) / pair : 0;
+      int incl = cnt;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) B.warp_sum[warp] = incl;
+      __syncthreads();
+      int before = base, total = 0;
+      for (int i = 0; i < kTcThreads / 32; ++i) {
+        if (i < warp) before += B.warp_sum[i];
+        total += B.warp_sum[i];
+      }
+      const int at = item - (before + incl - cnt);
+      if (at >= 0 && at < cnt) {
+        B.found_b = b;
+        B.found_t = cnt - 1 - at;
+      }
+      base += total;
+      __syncthreads();
+      if (item < base) break;
     }
-    if (lane == 31) B.warp_sum[warp] = incl;
-    __syncthreads();
-    int before = base, total = 0;
-    for (int i = 0; i < kTcThreads / 32; ++i) {
-      if (i < warp) before += B.warp_sum[i];
-      total += B.warp_sum[i];
-    }
-    const int at = item - (before + incl - cnt);
-    if (at >= 0 && at < cnt) {
-      B.found_b = b;
-      B.found_t = cnt - 1 - at;
-    }
-    base += total;
-    __syncthreads();
-    if (item < base) break;
+    b = B.found_b;
+    ft = B.found_t;
   }
-  const int b = B.found_b;
   if (b < 0) {
     if (w.parts && split == 0 && threadIdx.x == 0) w.rows[unit] = make_int2(0, 0);
     return;
   }
   const SeqView s = seq_view(a.kv.q_start, a.kv.kv_len, b, a.kv.per, a.T, a.kv.cap);
-  const int tok0 = B.found_t * pair;
+  const int tok0 = ft * pair;
   const int nq = s.m - tok0 > w.tokens ? 2 : 1;
   const int base = s.n - s.m;
   const int p0 = base + tok0, p1 = base + min(s.m, tok0 + pair) - 1;
