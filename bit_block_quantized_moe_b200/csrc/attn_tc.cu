@@ -27,7 +27,7 @@
 #include <algorithm>
 
 #include "attn.cuh"
-#include "tc.cuh"
+#include "half.cuh"
 
 namespace moe {
 namespace {

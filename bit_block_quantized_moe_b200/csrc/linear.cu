@@ -23,7 +23,7 @@
 #include <algorithm>
 
 #include "kernels.cuh"
-#include "tc.cuh"
+#include "half.cuh"
 
 namespace moe {
 namespace {

@@ -17,7 +17,7 @@
 #include <algorithm>
 
 #include "attn.cuh"
-#include "sync.cuh"
+#include "half.cuh"
 
 namespace moe {
 namespace {
