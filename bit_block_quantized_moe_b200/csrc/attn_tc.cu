@@ -237,8 +237,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   if (b < 0) {
     if (w.parts && split == 0 && threadIdx.x == 0) w.rows[unit] = make_int2(0, 0);
-    return;
+    return;  // with the whole cluster, which has one item
   }
+  // A CTA without key tiles comes to the join almost at once: before it writes the others' shared memory they have to
+  // run, which it waits for there.
+  const bool clustered = splits > 1 && !w.parts;
+  if (clustered) cluster_started();
   const SeqView s = seq_view(a.kv.q_start, a.kv.kv_len, b, a.kv.per, a.T, a.kv.cap);
   const int tok0 = ft * pair;
   const int nq = s.m - tok0 > w.tokens ? 2 : 1;
@@ -423,7 +427,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   if (splits > 1) {  // the meetings of the parts, below
     __syncthreads();
-    if (!w.parts) cluster_meet();
+    if (clustered) {
+      cluster_wait_started();
+      cluster_meet();
+    }
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -591,6 +598,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       constexpr int kQuads = D / 4;
       const int log_own = 6 + nq - w.log_splits, own = 1 << log_own;  // rows a CTA finishes: nq * 128 / splits
       __syncthreads();  // no product or copy needs the stages any more
+      if (clustered) cluster_wait_started();
       if ((warp >> 2) < nq) {
         const int i = warp >> 2, row = threadIdx.x & 127, r = i * 128 + row;
         const uint32_t to = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + C::kO + i * D;
@@ -631,7 +639,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bulk_store(parts + ((size_t)split * 256 + r) * D, smem_u32(mine + (size_t)r * D), (uint32_t)(rows * D * 4));
       }
       __syncwarp();
-      if (!w.parts) cluster_meet();  // releases and acquires what went to the workspace too
+      if (clustered) cluster_meet();  // releases and acquires what went to the workspace too
       const TcRows where{a.out + ((size_t)s.q0 * a.H + (size_t)hv * a.G) * D, a.H, a.G, tok0, w.tokens, s.m, nq};
       if (w.parts)
         ;  // attn_tc_join_kernel
