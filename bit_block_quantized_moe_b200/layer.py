@@ -1,10 +1,24 @@
 """Q2MoeLayer: owns the device buffers of one layer and calls the C ABI."""
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
 from . import binding as B
+
+
+def stream_made_current(stream, device):
+    """Context in which the `stream` argument of a call (None: as it is, a raw handle, or an object that has one) is the
+    current stream of `device`, so that buffers made there are filled, and freed, in its order."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        # 0 and 1 are names of the legacy default stream
+        stream = torch.cuda.ExternalStream(handle, device) if handle > 1 else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 class Q2MoeLayer:
@@ -56,15 +70,36 @@ class Q2MoeLayer:
         torch.cuda.synchronize(self.device)
 
     def reserve(self, T: int):
+        """Workspace for calls of up to T tokens, ready for a call on any stream when this returns.  (While a stream is
+        captured it is filled by the graph.)"""
+        old = self.workspace
+        if self._grow(T) and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.synchronize(self.device)  # the new one is filled, and calls on any stream are done with the old
+        del old
+
+    def _grow(self, T: int) -> bool:
+        """Makes a larger workspace, filled in the order of the current stream."""
+        if T <= self._ws_T:
+            return False
+        nbytes = B.moe_workspace_bytes(self.dims, T)
+        if self.workspace is not None:
+            # A call on this stream replaces the workspace that it shares with the calls before it, which it follows.
+            # Made on another stream, it could be reused there while they still run.
+            self.workspace.record_stream(torch.cuda.current_stream(self.device))
+        self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        self._ws_T = T
+        return True
+
+    def _prepare(self, T: int, stream):
+        """A call of T tokens on `stream` is about to run."""
         if T > self._ws_T:
-            nbytes = B.moe_workspace_bytes(self.dims, T)
-            self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-            self._ws_T = T
+            with stream_made_current(stream, self.device):
+                self._grow(T)
 
     def forward(self, x, out=None, topk_idx=None, topk_w=None, stream=None):
         """x: [T, hidden] bf16 (torch.bfloat16 or int16 bit patterns) on device."""
         T = x.shape[0]
-        self.reserve(T)
+        self._prepare(T, stream)
         if out is None:
             out = torch.empty_like(x)
         B.moe_layer_forward(self.dims, x, self.router_w, self.router_b, self.experts, self.shared, out, T,
@@ -75,7 +110,7 @@ class Q2MoeLayer:
         """x_host: [T <= 8, hidden] bf16 bit patterns in page-locked host memory; the output goes to out_host
         (page-locked, allocated if None), complete once the stream has passed the call."""
         T = x_host.shape[0]
-        self.reserve(T)
+        self._prepare(T, stream)
         if out_host is None:
             out_host = torch.empty(x_host.shape, dtype=x_host.dtype).pin_memory()
         B.moe_layer_forward_host(self.dims, x_host, self.router_w, self.router_b, self.experts, self.shared, out_host,
@@ -85,14 +120,14 @@ class Q2MoeLayer:
     def forward_residual(self, x_norm, resid, x_norm_out, eps=1e-6, topk_idx=None, topk_w=None, stream=None):
         """One stacked layer: resid += layer(x_norm); x_norm_out = bf16(RMSNorm(resid))."""
         T = x_norm.shape[0]
-        self.reserve(T)
+        self._prepare(T, stream)
         B.moe_layer_forward_residual(self.dims, x_norm, self.router_w, self.router_b, self.experts, self.shared, resid,
                                      x_norm_out, T, self.workspace, eps, topk_idx, topk_w, stream)
         return x_norm_out
 
     def experts_forward(self, x, topk_idx, topk_w, out=None, stream=None):
         T = x.shape[0]
-        self.reserve(T)
+        self._prepare(T, stream)
         if out is None:
             out = torch.empty_like(x)
         B.moe_experts_forward(self.dims, x, topk_idx, topk_w, self.experts, self.shared, out, T, self.workspace,
@@ -101,7 +136,7 @@ class Q2MoeLayer:
 
     def route(self, x, topk_idx=None, topk_w=None, stream=None):
         T = x.shape[0]
-        self.reserve(T)
+        self._prepare(T, stream)
         k = self.dims.top_k
         if topk_idx is None:
             topk_idx = torch.empty((T, k), dtype=torch.int32, device=self.device)
