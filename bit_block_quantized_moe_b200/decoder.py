@@ -4,7 +4,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
-from .layer import Q2MoeLayer
+from .layer import Q2MoeLayer, stream_made_current
 
 
 class PagedKvCache:
@@ -71,15 +71,31 @@ class Q2DecoderLayer:
 
     def reserve(self, T: int, n_seqs: int):
         """Activations and workspace for calls of up to T tokens and n_seqs sequences, as for Q2MoeLayer shared by all
-        calls of this layer: two that can run at the same time need a layer each."""
+        calls of this layer: two that can run at the same time need a layer each.  Ready for a call on any stream when
+        this returns."""
+        old = self._buffers()
+        if self._grow(T, n_seqs):
+            torch.cuda.synchronize(self.moe.device)  # they are filled, and calls on any stream are done with the old
+        del old
+
+    def _buffers(self):
+        return (self._qkv, self._q, self._o, self._mid, self._ws, self.moe.workspace) if self._reserved[0] >= 0 else ()
+
+    def _grow(self, T: int, n_seqs: int) -> bool:
+        """Makes larger buffers, filled in the order of the current stream."""
         if T <= self._reserved[0] and n_seqs <= self._reserved[1]:
-            return
+            return False
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("reserve the largest call before capturing one")
+        old = self._buffers()
         if self._captured:  # a graph that still reads and writes the smaller buffers
-            self._kept.append((self._qkv, self._q, self._o, self._mid, self._ws, self.moe.workspace))
+            self._kept.append(old)
         T, n_seqs = max(T, self._reserved[0]), max(n_seqs, self._reserved[1])
         d, hidden, dev = self.cache.dims, self.moe.dims.hidden, self.moe.device
+        for t in old[:5]:
+            # a call on this stream follows the calls before it, with which it shared these; made on another stream,
+            # they could be reused there while those still run
+            t.record_stream(torch.cuda.current_stream(dev))
         rows = lambda n: torch.empty((T, n), dtype=torch.bfloat16, device=dev)  # noqa: E731
         self._qkv, self._q, self._o = rows(self.w_qkv.shape[0]), rows(self.w_out.shape[1]), rows(self.w_out.shape[1])
         self._mid = rows(hidden)
@@ -87,8 +103,17 @@ class Q2DecoderLayer:
                                    B.moe_linear_workspace_bytes(T, hidden, self.w_qkv.shape[0]),
                                    B.moe_linear_workspace_bytes(T, self.w_out.shape[1], hidden)),
                                dtype=torch.uint8, device=dev)
-        self.moe.reserve(T)
+        self.moe._grow(T)
         self._reserved = (T, n_seqs)
+        return True
+
+    def _prepare(self, T: int, n_seqs: int, stream):
+        """A call is about to run on `stream`."""
+        if stream is not None and B._stream(stream) != B._stream(None):
+            with stream_made_current(stream, self.moe.device):
+                return self._prepare(T, n_seqs, None)
+        self._grow(T, n_seqs)
+        self._captured = self._captured or torch.cuda.is_current_stream_capturing()
 
     def forward(self, x_norm, resid, x_norm_out, kv_len, page_table, q_start=None, stream=None):
         """x_norm [T, hidden] bf16: the RMSNorm of resid [T, hidden] fp32 (moe_rmsnorm_residual, or the layer before);
@@ -98,8 +123,7 @@ class Q2DecoderLayer:
         T = x_norm.shape[0]
         if T == 0:
             return x_norm_out
-        self.reserve(T, kv_len.shape[0])
-        self._captured = self._captured or torch.cuda.is_current_stream_capturing()
+        self._prepare(T, kv_len.shape[0], stream)
         c, ws = self.cache, self._ws
         x = x_norm if x_norm.dtype == torch.bfloat16 else x_norm.view(torch.bfloat16)
         qkv, q, o, mid = self._qkv[:T], self._q[:T], self._o[:T], self._mid[:T]

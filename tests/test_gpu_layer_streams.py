@@ -86,3 +86,107 @@ def test_moe_layer_reserved_here_and_called_there(M):
     layer.forward(x, out=out, stream=side)
     side.synchronize()
     assert torch.equal(out, want)
+
+
+# ---- the decoder layer ---------------------------------------------------------------------------------------------
+def decoder_calls(layer, stream, clean):
+    """A prompt and windows of two sequences, each call larger than the buffers of the last or smaller: the residuals,
+    next inputs and the cache."""
+    import bit_block_quantized_moe_b200 as M
+
+    g = torch.Generator(device="cuda").manual_seed(17)
+    hidden, lens, steps = layer.moe.dims.hidden, [600, 2500], []
+    for s, n in enumerate(lens):
+        layer.cache.grow(s, n)
+    layer.cache.k.normal_(generator=g)
+    layer.cache.v.normal_(generator=g)
+    for m in (1, 3, 40, 2, 200):  # the first one takes parts of a cut group, whose counts have to be zero
+        resid = torch.randn((2 * m, hidden), generator=g, device="cuda")
+        x = torch.empty((2 * m, hidden), dtype=torch.bfloat16, device="cuda")
+        M.moe_rmsnorm_residual(resid, None, x, 2 * m, hidden, 1e-6)
+        steps.append((x, resid, torch.empty_like(x)))
+    kv_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    table = layer.cache.table(range(2))
+    torch.cuda.synchronize()
+    clean()
+    for x, resid, x_next in steps:
+        layer.forward(x, resid, x_next, kv_len, table, stream=stream)
+        for n in (1 << 10, 1 << 16, 1 << 20, 1 << 22):
+            torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")
+    return [t for _, a, b in steps for t in (a, b)] + [layer.cache.k, layer.cache.v]
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_decoder_layer_on_another_stream(M, raw):
+    from test_gpu_decoder_layer import build
+
+    alone = build(M, seed=2, pages=200)
+    want = decoder_calls(alone, None, lambda: None)
+    alone.check_status()
+    layer, side = build(M, seed=2, pages=200), torch.cuda.Stream()
+
+    def busy():
+        soil(side)
+        soil(torch.cuda.current_stream())
+        torch.cuda._sleep(BUSY)
+
+    got = decoder_calls(layer, side.cuda_stream if raw else side, busy)
+    side.synchronize()
+    assert not torch.cuda.current_stream().query()  # the calls waited for nothing there
+    layer.check_status(side)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    torch.cuda.synchronize()
+
+
+def test_decoder_layer_reserved_here_and_called_there(M):
+    from test_gpu_decoder_layer import build
+
+    want = decoder_calls(build(M, seed=2, pages=200), None, lambda: None)
+    layer, side = build(M, seed=2, pages=200), torch.cuda.Stream()
+
+    def reserve():
+        soil(torch.cuda.current_stream())
+        torch.cuda._sleep(BUSY)
+        layer.reserve(400, 2)
+
+    got = decoder_calls(layer, side, reserve)
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_decoder_layer_captured_on_a_stream_that_is_not_current(M):
+    """The larger call after the capture leaves the graph its buffers, though the capturing stream was only an argument."""
+    from test_gpu_decoder_layer import build
+
+    layer, side = build(M, seed=5), torch.cuda.Stream()
+    hidden = layer.moe.dims.hidden
+    g = torch.Generator(device="cuda").manual_seed(3)
+    layer.cache.grow(0, 300)
+    table = layer.cache.table([0])
+    start = torch.randn((1, hidden), generator=g, device="cuda")
+    resid, kv_len = start.clone(), torch.tensor([300], dtype=torch.int32, device="cuda")
+    x, x_next = (torch.empty((1, hidden), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    M.moe_rmsnorm_residual(resid, None, x, 1, hidden, 1e-6)
+    layer.reserve(1, 1)
+    layer.forward(x, resid, x_next, kv_len, table, stream=side)
+    torch.cuda.synchronize()
+    want = resid.clone(), x_next.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        graph.capture_begin()
+        with torch.cuda.stream(torch.cuda.Stream()):
+            layer.forward(x, resid, x_next, kv_len, table, stream=side)
+        graph.capture_end()
+    assert layer._captured
+    many = torch.zeros((300, hidden), device="cuda")
+    x_many = torch.zeros((300, hidden), dtype=torch.bfloat16, device="cuda")
+    layer.forward(x_many, many, torch.empty_like(x_many), kv_len, table)
+    held = [torch.full((300, hidden), 7.0, device="cuda") for _ in range(64)]
+    layer.cache.k.zero_(), layer.cache.v.zero_()
+    resid.copy_(start)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(resid, want[0]) and torch.equal(x_next, want[1])
+    assert all((h == 7.0).all() for h in held)

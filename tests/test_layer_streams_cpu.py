@@ -44,8 +44,8 @@ class Cuda:
     def call(self, name):
         """A stand-in of a call of the library: its stream, and the tensors that it was given."""
         def called(*a, **kw):
-            stream = kw.get("stream", next((x for x in reversed(a) if isinstance(x, Stream)), None))
-            self.log.append((name, self.current if stream is None else stream.cuda_stream,
+            stream = kw["stream"] if "stream" in kw else a[-1]
+            self.log.append((name, self.current if stream is None else getattr(stream, "cuda_stream", stream),
                              [id(x) for x in a if isinstance(x, torch.Tensor)]))
         return called
 
@@ -63,6 +63,7 @@ class Stream:
 @pytest.fixture
 def cuda(monkeypatch):
     c = Cuda(monkeypatch)
+    monkeypatch.setattr(B, "_stream", lambda s, dev=None: c.current if s is None else getattr(s, "cuda_stream", s))
     monkeypatch.setattr(B, "moe_workspace_bytes", lambda dims, T: 16 * (T + 1))
     for name in ("moe_layer_forward", "moe_layer_forward_host", "moe_layer_forward_residual", "moe_experts_forward",
                  "moe_route"):
@@ -123,3 +124,87 @@ def test_streams_given_as_handles(cuda):
         with stream_made_current(given, torch.device("cpu")):
             assert cuda.current == want
     assert cuda.current == MAIN
+
+
+# ---- the decoder layer ---------------------------------------------------------------------------------------------
+PARTS = ("moe_linear", "moe_qk_norm_rope", "moe_attn_forward", "moe_linear", "moe_rmsnorm_residual",
+         "moe_layer_forward_residual")
+BUFFERS = ("_qkv", "_q", "_o", "_mid", "_ws")
+
+
+@pytest.fixture
+def decoder(cuda, monkeypatch):
+    from bit_block_quantized_moe_b200.decoder import Q2DecoderLayer
+
+    for name in set(PARTS):
+        monkeypatch.setattr(B, name, cuda.call(name))
+    monkeypatch.setattr(B, "moe_attn_workspace_bytes", lambda dims, n_seqs, T: 64 * n_seqs + T)
+    monkeypatch.setattr(B, "moe_linear_workspace_bytes", lambda T, K, N: 64)
+    layer = object.__new__(Q2DecoderLayer)
+
+    class Cache:
+        dims, k, v = B.moe_attn_dims(2, 1, 64, 16), None, None
+
+    layer.__dict__.update(moe=moe_layer(), cache=Cache, w_qkv=torch.ones(256, 64), w_out=torch.ones(64, 128), b_qkv=None,
+                          q_gain=None, k_gain=None, rope=None, window=0, n_sinks=0, eps=1e-6, _reserved=(-1, -1),
+                          _captured=False, _kept=[])
+
+    def call(T, stream, n_seqs=1):
+        x = torch.ones((T, 64), dtype=torch.bfloat16)
+        layer.forward(x, torch.ones(T, 64), x, torch.ones(n_seqs, dtype=torch.int32), None, stream=stream)
+
+    return layer, call
+
+
+def buffers(layer):
+    return [getattr(layer, n) for n in BUFFERS] + [layer.moe.workspace]
+
+
+def test_decoder_buffers_are_made_on_the_stream_of_the_call_that_needs_them(cuda, decoder):
+    layer, call = decoder
+    call(3, Stream(0x20))
+    first = buffers(layer)
+    assert [cuda.made(t) for t in first] == [0x20] * 6 and cuda.current == MAIN
+    assert [(e[0], e[1]) for e in cuda.log if e[0] in PARTS] == [(n, 0x20) for n in PARTS]
+    call(2, Stream(0x20))
+    assert all(a is b for a, b in zip(buffers(layer), first))
+    call(5, Stream(0x30))
+    second = buffers(layer)
+    assert [cuda.made(t) for t in second] == [0x30] * 6
+    assert all(("keep", id(t), 0x30) in cuda.log for t in first)
+    call(5, 0x40, n_seqs=4)  # a raw handle, and more sequences alone
+    third = buffers(layer)
+    assert [cuda.made(t) for t in third[:5]] == [0x40] * 5 and third[5] is second[5]
+    assert all(("keep", id(t), 0x40) in cuda.log for t in second[:5])
+    call(9, None)
+    assert [cuda.made(t) for t in buffers(layer)] == [MAIN] * 6
+    assert ("synchronize",) not in cuda.log
+
+
+def test_decoder_reserve_is_complete_when_it_returns(cuda, decoder):
+    layer, _ = decoder
+    layer.reserve(4, 2)
+    assert cuda.log[-1] == ("synchronize",)
+    count = len(cuda.log)
+    layer.reserve(4, 1)
+    assert len(cuda.log) == count
+    layer.reserve(4, 3)
+    assert cuda.log[-1] == ("synchronize",)
+
+
+@pytest.mark.parametrize("own", [False, True])
+def test_decoder_knows_that_its_stream_is_captured(cuda, decoder, own):
+    """The capture is of the stream that the call runs on, be it the current one or not."""
+    layer, call = decoder
+    stream = Stream(0x20) if own else None
+    call(3, stream)
+    assert not layer._captured
+    cuda.capturing = 0x20 if own else MAIN
+    with pytest.raises(RuntimeError, match="reserve"):
+        call(4, stream)
+    call(3, stream)
+    assert layer._captured
+    cuda.capturing = False
+    first = buffers(layer)
+    call(4, stream)
+    assert len(layer._kept) == 1 and all(a is b for a, b in zip(layer._kept[0], first))
