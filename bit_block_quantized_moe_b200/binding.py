@@ -132,6 +132,11 @@ def lib():
         L.moe_qk_norm_rope.argtypes = [A, P, i64, P, P, f32, ctypes.POINTER(moe_rope), C, S, i32, P, P, sz, P]
         L.moe_attn_forward.restype = ctypes.c_int
         L.moe_attn_forward.argtypes = [A, P, i64, C, S, i32, f32, i32, i32, P, P, sz, P]
+        # of the CUDA runtime that the library is linked to
+        L.cudaStreamIsCapturing.restype = ctypes.c_int
+        L.cudaStreamIsCapturing.argtypes = [P, ctypes.POINTER(ctypes.c_int)]
+        L.cudaGetLastError.restype = ctypes.c_int
+        L.cudaGetLastError.argtypes = []
         L.moe_trace_kernel.restype = ctypes.c_int
         L.moe_trace_kernel.argtypes = [i32, P, P]
         L.moe_set_cold_expert_tokens.restype = ctypes.c_int
@@ -159,6 +164,16 @@ def _stream(stream, dev=None):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def stream_captured(stream=None) -> bool:
+    """Whether work on `stream` (None: the current one) goes into a graph."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    status = ctypes.c_int(0)
+    if lib().cudaStreamIsCapturing(_stream(stream), ctypes.byref(status)) != 0:
+        lib().cudaGetLastError()  # the legacy stream while another one is captured: the call itself will say so
+    return status.value != 0
 
 
 def _check(code: int, what: str):

@@ -73,13 +73,13 @@ class Q2DecoderLayer:
         """Activations and workspace for calls of up to T tokens and n_seqs sequences, as for Q2MoeLayer shared by all
         calls of this layer: two that can run at the same time need a layer each.  Ready for a call on any stream when
         this returns."""
-        old = self._buffers()
+        old = (*self._buffers(), self.moe.workspace)
         if self._grow(T, n_seqs):
             torch.cuda.synchronize(self.moe.device)  # they are filled, and calls on any stream are done with the old
         del old
 
     def _buffers(self):
-        return (self._qkv, self._q, self._o, self._mid, self._ws, self.moe.workspace) if self._reserved[0] >= 0 else ()
+        return (self._qkv, self._q, self._o, self._mid, self._ws) if self._reserved[0] >= 0 else ()
 
     def _grow(self, T: int, n_seqs: int) -> bool:
         """Makes larger buffers, filled in the order of the current stream."""
@@ -92,7 +92,7 @@ class Q2DecoderLayer:
             self._kept.append(old)
         T, n_seqs = max(T, self._reserved[0]), max(n_seqs, self._reserved[1])
         d, hidden, dev = self.cache.dims, self.moe.dims.hidden, self.moe.device
-        for t in old[:5]:
+        for t in old:
             # a call on this stream follows the calls before it, with which it shared these; made on another stream,
             # they could be reused there while those still run
             t.record_stream(torch.cuda.current_stream(dev))
@@ -109,11 +109,10 @@ class Q2DecoderLayer:
 
     def _prepare(self, T: int, n_seqs: int, stream):
         """A call is about to run on `stream`."""
-        if stream is not None and B._stream(stream) != B._stream(None):
+        if T > self._reserved[0] or n_seqs > self._reserved[1]:
             with stream_made_current(stream, self.moe.device):
-                return self._prepare(T, n_seqs, None)
-        self._grow(T, n_seqs)
-        self._captured = self._captured or torch.cuda.is_current_stream_capturing()
+                self._grow(T, n_seqs)
+        self._captured = self._captured or B.stream_captured(stream)
 
     def forward(self, x_norm, resid, x_norm_out, kv_len, page_table, q_start=None, stream=None):
         """x_norm [T, hidden] bf16: the RMSNorm of resid [T, hidden] fp32 (moe_rmsnorm_residual, or the layer before);

@@ -45,6 +45,7 @@ class Q2MoeLayer:
         self._pack(shared_canon, 1, ce, self.shared)
         self.workspace = None
         self._ws_T = -1
+        self._captured, self._kept = False, []
         if max_tokens:
             self.reserve(max_tokens)
 
@@ -82,6 +83,8 @@ class Q2MoeLayer:
         if T <= self._ws_T:
             return False
         nbytes = B.moe_workspace_bytes(self.dims, T)
+        if self._captured:  # a graph that still uses the smaller one
+            self._kept.append(self.workspace)
         if self.workspace is not None:
             # A call on this stream replaces the workspace that it shares with the calls before it, which it follows.
             # Made on another stream, it could be reused there while they still run.
@@ -91,10 +94,11 @@ class Q2MoeLayer:
         return True
 
     def _prepare(self, T: int, stream):
-        """A call of T tokens on `stream` is about to run."""
+        """A call of T tokens is about to run on `stream`."""
         if T > self._ws_T:
             with stream_made_current(stream, self.device):
                 self._grow(T)
+        self._captured = self._captured or B.stream_captured(stream)
 
     def forward(self, x, out=None, topk_idx=None, topk_w=None, stream=None):
         """x: [T, hidden] bf16 (torch.bfloat16 or int16 bit patterns) on device."""

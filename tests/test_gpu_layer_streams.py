@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from bit_block_quantized_moe_b200 import binding
 from gen import CONFIGS, make_layer, make_x
 
 pytestmark = pytest.mark.gpu
@@ -190,3 +191,47 @@ def test_decoder_layer_captured_on_a_stream_that_is_not_current(M):
     torch.cuda.synchronize()
     assert torch.equal(resid, want[0]) and torch.equal(x_next, want[1])
     assert all((h == 7.0).all() for h in held)
+
+
+def test_a_graph_keeps_the_moe_workspace_of_its_calls(M):
+    """The MoE half called by itself with more tokens: graphs of it, and of the decoder layer, keep what they use."""
+    from test_gpu_decoder_layer import build
+
+    layer = build(M, seed=6)
+    hidden = layer.moe.dims.hidden
+    g = torch.Generator(device="cuda").manual_seed(4)
+    layer.cache.grow(0, 100)
+    table, kv_len = layer.cache.table([0]), torch.tensor([100], dtype=torch.int32, device="cuda")
+    start = torch.randn((1, hidden), generator=g, device="cuda")
+    resid = start.clone()
+    x, x_next, y = (torch.empty((1, hidden), dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    M.moe_rmsnorm_residual(resid, None, x, 1, hidden, 1e-6)
+
+    def step():
+        layer.forward(x, resid, x_next, kv_len, table)
+        layer.moe.forward(x, out=y)
+
+    step()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (resid, x_next, y)]
+    assert not binding.stream_captured() and not layer.moe._captured
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        assert binding.stream_captured() and binding.stream_captured(torch.cuda.current_stream())
+        step()
+    assert layer.moe._captured
+    many = torch.zeros((500, hidden), dtype=torch.bfloat16, device="cuda")
+    size = layer.moe.workspace.numel()
+    layer.moe.forward(many)
+    assert layer.moe.workspace.numel() > size
+    held = [torch.full((size,), 0xff, dtype=torch.uint8, device="cuda") for _ in range(32)]
+    for _ in range(2):
+        resid.copy_(start)
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((resid, x_next, y), want):
+            assert torch.equal(a, b)
+        assert all((h == 0xff).all() for h in held)
+    layer.check_status()
+

@@ -64,6 +64,7 @@ class Stream:
 def cuda(monkeypatch):
     c = Cuda(monkeypatch)
     monkeypatch.setattr(B, "_stream", lambda s, dev=None: c.current if s is None else getattr(s, "cuda_stream", s))
+    monkeypatch.setattr(B, "stream_captured", lambda s=None: bool(c.capturing) and B._stream(s) == c.capturing)
     monkeypatch.setattr(B, "moe_workspace_bytes", lambda dims, T: 16 * (T + 1))
     for name in ("moe_layer_forward", "moe_layer_forward_host", "moe_layer_forward_residual", "moe_experts_forward",
                  "moe_route"):
@@ -74,7 +75,7 @@ def cuda(monkeypatch):
 def moe_layer():
     layer = object.__new__(Q2MoeLayer)
     layer.__dict__.update(dims=B.moe_dims(64, 32, 4, 2), device=torch.device("cpu"), router_w=None, router_b=None,
-                          experts=None, shared=None, workspace=None, _ws_T=-1)
+                          experts=None, shared=None, workspace=None, _ws_T=-1, _captured=False, _kept=[])
     return layer
 
 
@@ -115,6 +116,25 @@ def test_moe_reserve_is_complete_when_it_returns(cuda):
     count = cuda.log.count(("synchronize",))
     layer.reserve(6)
     assert cuda.log.count(("synchronize",)) == count and layer.workspace.numel() == 16 * 7
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("own", [False, True])
+def test_moe_graphs_keep_the_workspace_of_their_call(cuda, call, own):
+    """A larger call, whoever makes it, takes a workspace of its own when a graph uses the smaller one."""
+    layer, stream = moe_layer(), Stream(0x20) if own else None
+    x, many = (torch.ones((T, 64), dtype=torch.bfloat16) for T in (3, 9))
+    CALLS[call](layer, x, stream)
+    CALLS[call](layer, many, stream)
+    assert layer._kept == []  # no graph: nothing to keep
+    cuda.capturing = 0x20 if own else MAIN
+    CALLS[call](layer, x, stream)
+    cuda.capturing = False
+    used = layer.workspace
+    layer.reserve(20)
+    assert len(layer._kept) == 1 and layer._kept[0] is used
+    CALLS[call](layer, torch.ones((30, 64), dtype=torch.bfloat16), None)
+    assert layer.workspace.numel() == 16 * 31
 
 
 def test_streams_given_as_handles(cuda):
