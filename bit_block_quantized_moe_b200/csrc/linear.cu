@@ -80,6 +80,28 @@ __device__ __forceinline__ bool ln_wait(uint64_t *bar, uint32_t parity, Bars &B,
   return true;
 }
 
+// gelu(z) = z/2 (1 + erf(z / sqrt 2)) = (z + a)/2 - a F(-a), a = |z|, with the normal distribution F: 1 + erf would lose
+// negative z (4% off at -5, nothing left at -5.6).  F(-a) = e^(-a^2/2) R(a), where R(a) = erfcx(a / sqrt 2)/2 falls from
+// 1/2 as slowly as 1/a and is t P(t) with t = 1 / (1 + 0.3 a): a polynomial of degree 7, fitted by reweighted least
+// squares to the smallest relative error (1.5e-7) over a <= 14, where F is below fp32's normal numbers.  Within
+// (a^2 + 10) 2^-23 of the result.  32768 x 512 x 2560, which the epilogue bounds, takes 154 us; 179 with erff, and 249
+// with erfcf, which does not cancel either.
+__device__ __forceinline__ float ln_gelu(float z) {
+  const float a = fminf(fabsf(z), 64.f);  // beyond, F is 0; infinities and NaN stay in the first term
+  float t, e;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(a, 0.3f, 1.f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * a * -0.72134752f));  // -log2(e) / 2
+  float p = 0.035674773f;
+  p = fmaf(p, t, -0.15720308f);
+  p = fmaf(p, t, 0.2063535f);
+  p = fmaf(p, t, -0.053683642f);
+  p = fmaf(p, t, 0.12856163f);
+  p = fmaf(p, t, 0.09991349f);
+  p = fmaf(p, t, 0.12075396f);
+  p = fmaf(p, t, 0.1196293f);
+  return fmaf(-(a * t), p * e, fmaf(0.5f, z, 0.5f * fabsf(z)));
+}
+
 // Finishes COUNT outputs i0, i0 + step, ... of sums z (with the bias in them), those with ok set: residuals are read
 // together, before the first store, which may go to the same memory.
 template <int COUNT>
@@ -89,7 +111,7 @@ __device__ __forceinline__ void ln_finish(const LnArgs &a, size_t i0, size_t ste
     for (int n = 0; n < COUNT; ++n) z[n] = __fdividef(z[n], 1.0f + __expf(-z[n]));
   } else if (a.act == MOE_ACT_GELU) {
 #pragma unroll
-    for (int n = 0; n < COUNT; ++n) z[n] = 0.5f * z[n] * (1.0f + erff(z[n] * 0.70710678118654752f));
+    for (int n = 0; n < COUNT; ++n) z[n] = ln_gelu(z[n]);
   }
   if (a.resid) {
     float r[COUNT];
