@@ -80,6 +80,15 @@ __device__ __forceinline__ bool ln_wait(uint64_t *bar, uint32_t parity, Bars &B,
   return true;
 }
 
+// silu(z) = z / (1 + e^-z) with a power that cannot overflow, e = e^-|z|: z / (1 + e), and z e / (1 + e) below zero (the
+// quotient by 1 + e^-z was cut to zero below -87, where the value is a normal number down to -91).
+__device__ __forceinline__ float ln_silu(float z) {
+  float e, r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(fabsf(z) * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return (z < 0.f ? z * e : z) * r;
+}
+
 // gelu(z) = z/2 (1 + erf(z / sqrt 2)) = (z + a)/2 - a F(-a), a = |z|, with the normal distribution F: 1 + erf would lose
 // negative z (4% off at -5, nothing left at -5.6).  F(-a) = e^(-a^2/2) R(a), where R(a) = erfcx(a / sqrt 2)/2 falls from
 // 1/2 as slowly as 1/a and is t P(t) with t = 1 / (1 + 0.3 a): a polynomial of degree 7, fitted by reweighted least
@@ -108,7 +117,7 @@ template <int COUNT>
 __device__ __forceinline__ void ln_finish(const LnArgs &a, size_t i0, size_t step, float (&z)[COUNT], int ok) {
   if (a.act == MOE_ACT_SILU) {
 #pragma unroll
-    for (int n = 0; n < COUNT; ++n) z[n] = __fdividef(z[n], 1.0f + __expf(-z[n]));
+    for (int n = 0; n < COUNT; ++n) z[n] = ln_silu(z[n]);
   } else if (a.act == MOE_ACT_GELU) {
 #pragma unroll
     for (int n = 0; n < COUNT; ++n) z[n] = ln_gelu(z[n]);

@@ -58,6 +58,17 @@ def test_gelu_keeps_its_relative_accuracy(M, wide):  # noqa: F811
     assert (err <= tol * ref.abs()).all(), f"worst {(err / (tol * ref.abs())).nan_to_num(0).max().item():.3g}"
 
 
+@pytest.mark.parametrize("wide", [False, True])
+def test_silu_keeps_its_relative_accuracy(M, wide):  # noqa: F811
+    """z / (1 + e^-z) down to where it leaves fp32's normal numbers (-91).  The power of two is within 2 units of the last
+    place (2^-23), its argument is rounded twice (|z| of 2^-24 each); a sum (1/2), a quotient (2), two products (1)."""
+    z = torch.linspace(-91, 91, 4001, device="cuda").bfloat16()
+    ref = z.double() / (1 + torch.exp(-z.double()))
+    tol = (z.double().abs() + 6) * 2.0 ** -23 + (0 if wide else 2.0 ** -8)
+    err = (activated(M, z, "silu", wide) - ref).abs()
+    assert (err <= tol * ref.abs()).all(), f"worst {(err / (tol * ref.abs())).nan_to_num(0).max().item():.3g}"
+
+
 @pytest.mark.parametrize("act", ["gelu", "silu"])
 @pytest.mark.parametrize("wide", [False, True])
 def test_activations_of_what_is_not_ordinary(M, act, wide):  # noqa: F811
