@@ -290,6 +290,8 @@ def moe_rmsnorm_residual(resid, y, x_norm, T: int, hidden: int, eps: float = 1e-
 MOE_ACT = {"none": 0, "silu": 1, "gelu": 2}
 
 
+# ctypes takes larger sizes modulo 2^32
+_INT32_END = 1 << 31
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _I32, _F32 = torch.int32, torch.float32
 
@@ -318,8 +320,8 @@ def moe_linear(x, w, out, workspace, bias=None, act="none", resid=None, stream=N
     T, K = x.shape
     N = w.shape[0]
     if w.shape[1] != K or out.shape != (T, N) or (bias is not None and (bias.numel() != N or bias.dtype != _F32)) or (
-            resid is not None and (resid.shape != (T, N) or resid.dtype != _F32)):
-        raise ValueError("moe_linear: shapes or types do not match")
+            resid is not None and (resid.shape != (T, N) or resid.dtype != _F32)) or max(T, K, N) >= _INT32_END:
+        raise ValueError("moe_linear: shapes or types do not match, or are too large")
     if act not in MOE_ACT or (out.dtype != _F32 if resid is not None else out.dtype not in _BF16):
         raise ValueError("moe_linear: out is bf16, or fp32 with a residual; act is none, silu or gelu")
     if x.stride(1) != 1 or not (w.is_contiguous() and out.is_contiguous() and (bias is None or bias.is_contiguous())
@@ -344,12 +346,13 @@ def moe_attn_workspace_bytes(dims: moe_attn_dims, n_seqs: int, max_T: int) -> in
 def _cache_and_batch(what, dims, k_cache, v_cache, kv_len, page_table, q_start):
     shape = k_cache.shape
     if shape[1:] != (dims.n_kv_heads, dims.page_size, dims.head_dim) or v_cache.shape != shape or not (
-            k_cache.is_contiguous() and v_cache.is_contiguous()):
+            k_cache.is_contiguous() and v_cache.is_contiguous()) or shape[0] >= _INT32_END:
         raise ValueError(f"{what}: k and v are contiguous [n_pages, n_kv_heads, page_size, head_dim]")
     n, pages = page_table.shape
     if kv_len.numel() != n or page_table.dtype != _I32 or kv_len.dtype != _I32 or not (
             page_table.is_contiguous() and kv_len.is_contiguous()) or (q_start is not None and (
-                q_start.numel() != n + 1 or q_start.dtype != _I32 or not q_start.is_contiguous())):
+                q_start.numel() != n + 1 or q_start.dtype != _I32 or not q_start.is_contiguous())) or (
+                    max(n, pages) >= _INT32_END):
         raise ValueError(f"{what}: kv_len [n_seqs], page_table [n_seqs, max_pages], q_start [n_seqs + 1], contiguous "
                          "int32")
     return (moe_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), shape[0]),
@@ -363,7 +366,7 @@ def _token_rows(what, t, heads, dim):
         ok = shape[1] == heads and shape[2] == dim and stride[2] == 1 and (heads == 1 or stride[1] == dim)
     else:
         ok = len(shape) == 2 and shape[1] == heads * dim and stride[1] == 1
-    if not ok:
+    if not ok or shape[0] >= _INT32_END:
         raise ValueError(f"{what} [T, {heads}, {dim}], every token contiguous")
     return stride[0] if shape[0] > 1 else heads * dim
 
@@ -390,6 +393,11 @@ def moe_qk_norm_rope(dims, qkv, q_out, k_cache, v_cache, kv_len, page_table, wor
     _check(code, what)
 
 
+def _tokens(n):
+    """A window or a number of sinks as the library takes it: 2^30 and more are all tokens, below 0 is refused there."""
+    return n if 0 <= n <= 1 << 30 else -1 if n < 0 else 1 << 30
+
+
 def moe_attn_forward(dims, q, out, k_cache, v_cache, kv_len, page_table, workspace, q_start=None, scale=None, window=0,
                      n_sinks=0, stream=None):
     """Attention of q [T, n_heads, head_dim] (tokens may be strided) over the paged cache; scale defaults to
@@ -402,8 +410,8 @@ def moe_attn_forward(dims, q, out, k_cache, v_cache, kv_len, page_table, workspa
     if out.shape[0] != T or out.numel() != T * dims.n_heads * dims.head_dim or not out.is_contiguous():
         raise ValueError("moe_attn_forward: out is contiguous [T, n_heads, head_dim]")
     code = lib().moe_attn_forward(ctypes.byref(dims), q.data_ptr(), ld, ctypes.byref(cache), ctypes.byref(batch), T,
-                                  dims.head_dim ** -0.5 if scale is None else scale, window, n_sinks, out.data_ptr(),
-                                  workspace.data_ptr(), workspace.nbytes, _stream(stream, dev))
+                                  dims.head_dim ** -0.5 if scale is None else scale, _tokens(window), _tokens(n_sinks),
+                                  out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream, dev))
     _check(code, what)
 
 
