@@ -18,8 +18,10 @@ constexpr size_t kWsHeader = 2048;  // the sticky status word; from byte 256 on 
 constexpr size_t kWsCounts = 256;
 static_assert(kWsCounts + kAttnShares * 4 <= kWsHeader, "the counts lie in the header");
 
+constexpr int32_t kMaxRows = 1 << 30;  // so that a row's number and a grid's step beyond it stay below 2^31
+
 static bool linear_dims_ok(int32_t T, int32_t K, int32_t N) {
-  return T >= 0 && T <= (1 << 30) && K >= 8 && K <= 65536 && K % 8 == 0 && N >= 1 && N <= 262144;
+  return T >= 0 && T <= kMaxRows && K >= 8 && K <= 65536 && K % 8 == 0 && N >= 1 && N <= 262144;
 }
 
 static bool attn_dims_ok(const moe_attn_dims *d) {
@@ -107,7 +109,7 @@ moe_status moe_rope_init(double theta, int32_t rotary_dim, moe_rope *rope) {
 }
 
 size_t moe_attn_workspace_bytes(const moe_attn_dims *dims, int32_t n_seqs, int32_t max_T) {
-  if (!attn_dims_ok(dims) || n_seqs < 1 || n_seqs > 65536 || max_T < 0) return 0;
+  if (!attn_dims_ok(dims) || n_seqs < 1 || n_seqs > 65536 || max_T < 0 || max_T > kMaxRows) return 0;
   return kWsHeader + attn_part_bytes(*dims, n_seqs, max_T);
 }
 
@@ -115,7 +117,7 @@ moe_status moe_qk_norm_rope(const moe_attn_dims *dims, const uint16_t *qkv, int6
                             const float *k_gain, float eps, const moe_rope *rope, const moe_kv_cache *cache,
                             const moe_kv_batch *batch, int32_t T, uint16_t *q_out, void *workspace, size_t ws_bytes,
                             moe_stream_t stream) {
-  if (!attn_dims_ok(dims) || T < 0 || !(eps >= 0.f)) return MOE_ERR_ARG;
+  if (!attn_dims_ok(dims) || T < 0 || T > kMaxRows || !(eps >= 0.f)) return MOE_ERR_ARG;
   if (rope && (rope->rotary_dim < 16 || rope->rotary_dim > dims->head_dim || rope->rotary_dim % 16)) return MOE_ERR_ARG;
   if (T == 0) return MOE_OK;
   if (!qkv || !q_out || !workspace) return MOE_ERR_ARG;
@@ -141,7 +143,7 @@ moe_status moe_qk_norm_rope(const moe_attn_dims *dims, const uint16_t *qkv, int6
 moe_status moe_attn_forward(const moe_attn_dims *dims, const uint16_t *q, int64_t ld_q, const moe_kv_cache *cache,
                             const moe_kv_batch *batch, int32_t T, float scale, int32_t window, int32_t n_sinks,
                             uint16_t *out, void *workspace, size_t ws_bytes, moe_stream_t stream) {
-  if (!attn_dims_ok(dims) || T < 0 || window < 0 || n_sinks < 0) return MOE_ERR_ARG;
+  if (!attn_dims_ok(dims) || T < 0 || T > kMaxRows || window < 0 || n_sinks < 0) return MOE_ERR_ARG;
   if (!isfinite(scale * 1.4426950408889634f)) return MOE_ERR_ARG;
   if (T == 0) return MOE_OK;
   if (!q || !out || !workspace) return MOE_ERR_ARG;

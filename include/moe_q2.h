@@ -334,7 +334,7 @@ typedef struct {
  * of n_seqs) and has kv_len[b] tokens in all, the new ones last: new token i of m
  * stands at position kv_len[b] - m + i.  The token at position p lives in page
  * page_table[b * max_pages + p / page_size], row p % page_size; entries past the
- * sequence's last page are never read.  1 <= n_seqs <= 65536, 1 <= max_pages,
+ * sequence's last page are never read.  1 <= n_seqs <= 65536, T <= 2^30, 1 <= max_pages,
  * max_pages * page_size <= 2^30.
  * A sequence with kv_len[b] = 0 is padding: its rows stand at negative positions.
  * Rows of no sequence (before q_start[0], at or after q_start[n_seqs]) are left as they
