@@ -339,10 +339,11 @@ typedef struct {
  * A sequence with kv_len[b] = 0 is padding: its rows stand at negative positions.
  * Rows of no sequence (before q_start[0], at or after q_start[n_seqs]) are left as they
  * were.  What the device finds wrong sets MOE_ERR_DEVICE in the workspace status: a
- * q_start pair that decreases or leaves [0, T] makes that sequence empty (rows that two
- * others then share may be left unwritten), a kv_len
- * outside [0, max_pages * page_size] counts as 0, and a token whose page is outside
- * [0, n_pages) is neither written nor seen. */
+ * q_start pair that decreases or leaves [0, T] makes that sequence empty (and where
+ * q_start decreases, rows of the others may be left as they were, and a row that two of
+ * them have may hold the result of either), a kv_len outside [0, max_pages * page_size]
+ * counts as 0, and a token whose page is outside [0, n_pages) is neither written nor
+ * seen. */
 typedef struct {
   int32_t n_seqs;
   int32_t max_pages;
