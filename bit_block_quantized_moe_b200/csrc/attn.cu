@@ -26,7 +26,7 @@
 // Bound: HBM; 64 ragged sequences of up to 16384 tokens (0.55 GB of keys and values) take 92 us, 93% of the copy rate.
 // Short calls are chains of waits: 500 tokens of one sequence 8 us.
 // Values of keys that no query of the window sees are masked in the registers that feed the product, so that nothing
-// behind them can reach an output.  Every wait is bounded (sync.cuh).
+// behind them can reach an output.  Every wait on memory is bounded (sync.cuh).
 #include <algorithm>
 
 #include "attn.cuh"
@@ -39,10 +39,13 @@ constexpr float kWinLazy = 8.0f;
 constexpr int kJoinParts = 12;  // more parts a group go to the second launch (4: 7 sequences 36 us instead of 25)
 // Windows of more than 32 rows go to the chunk kernel's tiles (32 x 8 tokens of 8 heads a group at 8192: 66 us there,
 // 131 here when this kernel still walked the keys once for 32 rows each), and those of 17 to 32 where it has five parts
-// or more for each sequence and key/value head (8 x 3 tokens at 16000: 36 us there, 46 here; 8 and 12 ragged up to 4000
-// 17 and 20, 25 and 23).  More sequences stay, as few or no parts cannot even out their lengths (64 x 3 ragged up to
-// 16384: 214 there, 135 here; but 64 x 3 at 1024 all 21 and 29), and so do 16 rows or fewer (8 x 2 ragged up to 16384:
-// 32 there, 21 here).
+// or more for each group, a sequence and key/value head.  Measured with windows of 3 tokens and 8 heads of 128 a group,
+// us there / here: 8 groups of 1000 tokens 12 / 17, of 4000 14 / 20, of 16000 23 / 30, ragged up to 4000 15 / 19, up to
+// 16000 22 / 24; 24 groups of 4000 21 / 25, of 16000 48 / 57, ragged up to 4000 21 / 24, but up to 16000 46 / 42; 29
+// groups 23 / 28, 57 / 66, 22 / 24, but 53 / 42.  More groups stay, as few or no parts cannot even out their lengths: 64
+// ragged up to 16000 115 / 69, 128 217 / 135, though with equal ones they would be quicker there too (128 of 1000 20 /
+// 29, of 4000 62 / 71, of 16000 219 / 235): the lengths are on the device.  16 rows or fewer stay as well (8 x 2 ragged
+// up to 16384: 32 there, 21 here).
 constexpr int kWinRows = 32, kWinFew = kAttnSms / 5;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {

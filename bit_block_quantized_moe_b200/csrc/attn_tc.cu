@@ -7,8 +7,9 @@
 //   P_i = 2^(scale S_i - m)    (one thread a row; bf16, over S_i in tensor memory)
 //   O_i += P_i V_j             (tensor memory, fp32)
 // The products of one row tile run under the softmax of the other.  A tile's chain of softmax (2300 cycles), P V and the
-// next Q K (700 and 620) paces it: 8192 tokens of 16 heads over 2 key/value heads take 252 us, 1095 TFLOP/s, with the
-// tensor core busy half of the time.  Slower: two threads a row (309 us, the exchange of the halves' maxima), a
+// next Q K (700 and 620) paces it: 8192 tokens of 16 heads over 2 key/value heads take 252 us from idle, 1095 TFLOP/s (281
+// and 980 in calls one behind another, at the clock that the power limit leaves), with the tensor core busy half of the
+// time.  Slower, from idle too: two threads a row (309 us, the exchange of the halves' maxima), a
 // quarter or half of the exponentials as polynomials on the FMA units (264, 302: the special function unit is not the
 // limit), weights begun before the maximum is known (262), steps of 64 keys with two places for S, so that the next Q K
 // runs under the softmax (394: 64 columns take the tensor core as long as 128).  m is the maximum seen so far, left as it is

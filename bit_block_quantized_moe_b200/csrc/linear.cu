@@ -17,9 +17,11 @@
 // 2.1e-6 of the result off and K = 4096 4.4e-6, which bf16 hides and fp32 does not; in slices of 512 it is 4.7e-7 at
 // any K (an fp32 product in software: 3.9e-7 and 6.1e-7), in slices of 256 2.4e-7 but 14% slower.
 // When the tiles alone leave SMs idle, a cluster of 2, 4 or 8 CTAs splits K: each sends the others their features'
-// parts through distributed shared memory and finishes its own, summed in rank order.  Every wait is bounded (sync.cuh).
-// Measured: 32768 x 2048 x 2560 231 us (1490 TFLOP/s; single CTAs 311); 1024 x 2048 x 2048 onto the residual 15.4 us,
-// of which 7 are launch, first loads and epilogue; 3 x 2048 x 2560 5.7 us against 1.6 for reading the weights.
+// parts through distributed shared memory and finishes its own, summed in rank order.  Every wait on a barrier in shared
+// memory is bounded (sync.cuh); CTAs of a cluster, which run together, meet without a limit.
+// Measured: 32768 x 2048 x 2560 260 us in calls one behind another (1320 TFLOP/s at the clock that the power limit leaves;
+// 231 us from idle, where single CTAs take 311); 1024 x 2048 x 2048 onto the residual 15.4 us, of which 7 are launch,
+// first loads and epilogue; 3 x 2048 x 2560 5.7 us against 1.6 for reading the weights.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -604,7 +606,8 @@ cudaError_t launch_linear(const uint16_t *x, int64_t ld, const uint16_t *w, cons
   a.status = status;
   // The tile that takes the fewest rounds of 64-wide chunks, each weighed by its products' cycles (64 columns are bound
   // by shared memory, 192 cycles); where the tiles leave half of the SMs idle, K split over a cluster (3 x 2048 x 2560:
-  // 7.4 us with the parts through global memory and a second launch, 6.5 so; 777 x 1160 x 1001 17.4 and 14.6).
+  // 7.4 us with the parts through global memory and a second launch, 6.5 so).  Between the two, as 777 x 1160 x 1001 with
+  // 104 tiles of 64 tokens, a CTA walks all of K alone.
   auto tiles = [&](int bn) { return (long long)a.n_ft * ((T + bn - 1) / bn); };
   int bn = 16;
   if (T > 16) {
