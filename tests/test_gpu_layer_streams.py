@@ -9,7 +9,7 @@ from gen import CONFIGS, make_layer, make_x
 
 pytestmark = pytest.mark.gpu
 
-BUSY = 50_000_000  # clock cycles: 25 ms, far more than all calls here together
+BUSY = 400_000_000  # clock cycles: 0.2 s, far more than all calls here together
 
 
 @pytest.fixture(scope="module")
